@@ -434,6 +434,87 @@ spops_status spops_delta_spmv(int64_t rows, int64_t cols, const int32_t* enc_off
                               spops_dtype val_type, const void* x, void* y, spops_dtype y_type,
                               void* hip_stream);
 
+/* ------------------------------------------------ low-rank adapters --
+ * Adapters of low rank beside a shared projection, many requests at once.
+ * Request i owns the tokens [offsets[i], offsets[i+1]) and the adapter
+ * a = adapter[i] of a pool; with k = ranks[a] (or rank) and s = scale[a]:
+ *   u = s A_a[:k] x,   y += B_a[:, :k] u        on the request's tokens.
+ * Tokens outside every request, and requests whose adapter is outside
+ * [0, adapters) or has no ranks, keep the base y.  Activations are
+ * feature-major (features x tokens, unit stride along the tokens).
+ *   dtype:   of every matrix (f32, f16 or bf16).  Sums and u are fp32; every
+ *            output value is rounded once.
+ *   tokens >= 0, requests >= 0, 1 <= adapters <= 65535, 1 <= rank <= 256,
+ *   features in 1..2^24.
+ *   A:       [adapters][rank][in_features]
+ *   B:       [adapters][out_features][rank]
+ *   offsets: [requests+1] int32, ascending (equal neighbours: an empty
+ *            request); adapter: [requests] int32.
+ *   ranks:   [adapters] int32 used ranks, clamped to [0, rank], or NULL (all
+ *            rank).  What A and B hold past an adapter's rank is not used.
+ *   scale:   [adapters] f32 or NULL (ones). */
+typedef struct spops_low_rank {
+  int64_t tokens, requests, adapters, rank, in_features, out_features;
+  spops_dtype dtype;
+  const void* A;
+  const void* B;
+  const int32_t* offsets;
+  const int32_t* adapter;
+  const int32_t* ranks;
+  const float* scale;
+} spops_low_rank;
+
+typedef enum spops_low_rank_op {
+  SPOPS_LOW_RANK_ADD = 0,
+  SPOPS_LOW_RANK_PROJECT = 1,
+  SPOPS_LOW_RANK_BACKWARD = 2
+} spops_low_rank_op;
+
+/* Workspace bytes of a call (only the sizes and dtype of L are read).  The
+ * workspace must be 256-byte aligned; its contents need no preparation. */
+spops_status spops_low_rank_workspace_size(const spops_low_rank* L, spops_low_rank_op op,
+                                           size_t* bytes);
+/* out = yt + adapters(xt).  yt, out: [out_features][tokens] (out may be yt);
+ * xt: [in_features][tokens]. */
+spops_status spops_low_rank_add(const spops_low_rank* L, const void* yt, int64_t ldy,
+                                const void* xt, int64_t ldx, void* out, int64_t ldo,
+                                void* workspace, size_t workspace_bytes, void* hip_stream);
+/* out = W xt + adapters(xt), the projection W [out_features][in_features]
+ * made in the same pass: for the few tokens of serving, where it is bound by
+ * reading W once.  Any number of tokens is correct; for long prompts a dense
+ * product followed by spops_low_rank_add is the faster way. */
+spops_status spops_low_rank_project(const spops_low_rank* L, const void* W, int64_t ldw,
+                                    const void* xt, int64_t ldx, void* out, int64_t ldo,
+                                    void* workspace, size_t workspace_bytes, void* hip_stream);
+/* Gradients of the adapters' part for dyt = dL/dy:
+ *   dxt [in_features][tokens] = sum s A^T B^T dy (zero on tokens without an
+ *       adapter; the projection's own W^T dy is not included),
+ *   dA [adapters][rank][in_features], dB [adapters][out_features][rank], both
+ *       written whole (zeros for unused adapters and past an adapter's rank). */
+spops_status spops_low_rank_backward(const spops_low_rank* L, const void* dyt, int64_t ldy,
+                                     const void* xt, int64_t ldx, void* dxt, int64_t lddx,
+                                     void* dA, void* dB, void* workspace, size_t workspace_bytes,
+                                     void* hip_stream);
+
+/* ------------------------------------------ gradient norm and clipping --
+ * norm = sqrt(sum over all tensors of grad^2) (fp64 sums, one f32 written at
+ * `norm`, device memory), c = min(1, max_norm / (norm + 1e-6)), and
+ * out[i] = c grad[i] in each tensor's dtype (fp32 product, one rounding).  out may be
+ * grad (in place; nothing is written where c is 1).  A norm that is NaN makes
+ * every value NaN.  `tensors` is a HOST array, read before the call returns;
+ * at most 2^20 tensors of at most 2^36 elements.  max_norm >= 0 (infinity
+ * allowed: the norm alone).  Outputs must not overlap other tensors' grads. */
+typedef struct spops_clip_tensor {
+  const void* grad;
+  void* out;
+  int64_t numel;
+  spops_dtype dtype;
+} spops_clip_tensor;
+spops_status spops_clip_grad_norm_workspace_size(int64_t count, size_t* bytes);
+spops_status spops_clip_grad_norm(const spops_clip_tensor* tensors, int64_t count,
+                                  double max_norm, float* norm, void* workspace,
+                                  size_t workspace_bytes, void* hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

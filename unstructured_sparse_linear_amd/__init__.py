@@ -7,7 +7,14 @@ behind the C ABI in include/spops.h (libspops.so); this package only
 marshals torch tensors into that ABI.  Nothing here falls back to another
 implementation: calls raise if libspops.so is missing.
 """
-from .adapter import MaskedAdam, SparseAdapter, SparsePattern, sparse_linear  # noqa: F401
+from .adapter import (  # noqa: F401
+    LowRankAdapters,
+    MaskedAdam,
+    SparseAdapter,
+    SparsePattern,
+    low_rank_linear,
+    sparse_linear,
+)
 from .spops import (  # noqa: F401
     SddmmPlan,
     SpmmPlan,
@@ -18,11 +25,15 @@ from .spops import (  # noqa: F401
     delta_encode,
     delta_spmv,
     clear_plan_caches,
+    clip_grad_norm,
     csr_add,
     csr_transpose,
     csr_transpose_permutation,
     csr_transpose_workspace,
     lib,
+    low_rank_add,
+    low_rank_backward,
+    low_rank_project,
     masked_adam,
     option,
     permute_values,
@@ -39,4 +50,5 @@ __all__ = ["spmm", "sddmm", "csr_add", "csr_transpose", "sort_rows_by_nnz", "Spm
            "sort_rows_workspace", "SparsePattern", "SparseAdapter", "sparse_linear", "cg",
            "masked_adam", "MaskedAdam", "DeltaMatrix", "delta_encode", "delta_spmv",
            "option", "set_option", "validate_csr", "InvalidCSR", "csr_transpose_permutation",
-           "permute_values"]
+           "permute_values", "low_rank_add", "low_rank_project", "low_rank_backward",
+           "low_rank_linear", "LowRankAdapters", "clip_grad_norm"]

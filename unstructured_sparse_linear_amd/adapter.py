@@ -24,8 +24,9 @@ from typing import Optional
 
 import torch
 
-from .spops import (SddmmPlan, SpmmPlan, csr_add, csr_transpose_permutation, masked_adam,
-                    permute_values, sddmm, sort_rows_by_nnz, spmm)
+from .spops import (SddmmPlan, SpmmPlan, csr_add, csr_transpose_permutation, low_rank_add,
+                    low_rank_backward, low_rank_project, masked_adam, permute_values, sddmm,
+                    sort_rows_by_nnz, spmm)
 
 
 class SparsePattern:
@@ -107,6 +108,64 @@ class SparseAdapter(torch.nn.Module):
     def merge_into(self, W: torch.Tensor) -> torch.Tensor:
         P = self.pattern
         return csr_add(self.values.detach(), P.ro, P.ri, P.ci, W)
+
+
+class _LowRankLinearFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, yt, xt, A, B, offsets, adapter, scale, ranks):
+        ctx.save_for_backward(xt, A, B, offsets, adapter, scale, ranks)
+        return low_rank_add(yt, xt, A, B, offsets, adapter, scale, ranks)
+
+    @staticmethod
+    def backward(ctx, dyt):
+        xt, A, B, offsets, adapter, scale, ranks = ctx.saved_tensors
+        dx = dA = dB = None
+        if any(ctx.needs_input_grad[1:4]):
+            dx, dA, dB = low_rank_backward(dyt.contiguous(), xt, A, B, offsets, adapter, scale,
+                                           ranks)
+        need = ctx.needs_input_grad
+        return (dyt if need[0] else None, dx if need[1] else None, dA if need[2] else None,
+                dB if need[3] else None, None, None, None, None)
+
+
+def low_rank_linear(yt: torch.Tensor, xt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                    offsets: torch.Tensor, adapter: torch.Tensor,
+                    scale: Optional[torch.Tensor] = None,
+                    ranks: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """low_rank_add, differentiable in yt, xt, A and B."""
+    return _LowRankLinearFn.apply(yt, xt, A, B, offsets, adapter, scale, ranks)
+
+
+class LowRankAdapters(torch.nn.Module):
+    """A pool of low-rank adapters on one layer of out_features x in_features:
+    A starts random, B at zero, so a new adapter changes nothing.
+
+      forward(yt, xt, offsets, adapter)   yt + the requests' adapters, for
+                                          training and prompts
+      project(W, xt, offsets, adapter)    W xt + the same in one pass over W,
+                                          for decode steps (no gradient)
+
+    yt may come from any layer on xt, a dense product or a SparseAdapter."""
+
+    def __init__(self, adapters: int, rank: int, in_features: int, out_features: int,
+                 scale: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None,
+                 dtype: torch.dtype = torch.float32, device="cuda"):
+        super().__init__()
+        A = torch.randn(adapters, rank, in_features, device=device) * in_features ** -0.5
+        self.A = torch.nn.Parameter(A.to(dtype))
+        self.B = torch.nn.Parameter(torch.zeros(adapters, out_features, rank, dtype=dtype,
+                                                device=device))
+        self.register_buffer("scale", scale)
+        self.register_buffer("ranks", ranks)
+
+    def forward(self, yt: torch.Tensor, xt: torch.Tensor, offsets: torch.Tensor,
+                adapter: torch.Tensor) -> torch.Tensor:
+        return low_rank_linear(yt, xt, self.A, self.B, offsets, adapter, self.scale, self.ranks)
+
+    @torch.no_grad()
+    def project(self, W: torch.Tensor, xt: torch.Tensor, offsets: torch.Tensor,
+                adapter: torch.Tensor) -> torch.Tensor:
+        return low_rank_project(W, xt, self.A, self.B, offsets, adapter, self.scale, self.ranks)
 
 
 class MaskedAdam(torch.optim.Optimizer):

@@ -1,4 +1,5 @@
-"""Build libspops.so (the HIP kernels and the C ABI) for gfx950 with hipcc.
+"""Build libspops.so (the HIP kernels and the C ABI) for gfx950 with hipcc, and
+_marshal.so (the compiled part of the Python binding) with the host compiler.
 
 Each .hip source under csrc/ is compiled to an object in parallel, then the
 objects are linked into libspops.so next to this file.  Always rebuilds.
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build", "spops")
 LIB = os.path.join(HERE, "libspops.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 CEILINGS_LIB = os.path.join(HERE, "libspops_ceilings.so")
 ARCH = os.environ.get("SPOPS_OFFLOAD_ARCH", "gfx950")
 
@@ -46,20 +49,56 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _run(cmd: list, what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stderr}")
+
+
+def _compile_marshal() -> str:
+    """csrc/marshal.cpp against the installed torch's headers; host code only."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(OBJDIR, "marshal.cpp.o")
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(_hipcc())))
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+          "-I", INCLUDE, "-isystem", inc,
+          "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+          "-isystem", os.path.join(rocm, "include"),
+          "-isystem", sysconfig.get_paths()["include"],
+          "-c", os.path.join(CSRC, "marshal.cpp"), "-o", obj], "g++ for marshal.cpp")
+    return obj
+
+
+def _link_marshal(obj: str) -> str:
+    import torch
+    tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MARSHAL + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:libspops.so", "-Wl,-rpath,$ORIGIN",
+          "-L", tlib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip",
+          f"-Wl,-rpath,{tlib}"], "link of _marshal.so")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(jobs: int | None = None, verbose: bool = False) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     jobs = jobs or min(len(srcs), os.cpu_count() or 4, 16)
     with cf.ThreadPoolExecutor(jobs) as ex:
+        marshal = ex.submit(_compile_marshal)
         objs = list(ex.map(_compile, srcs))
+        marshal_obj = marshal.result()
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_marshal(marshal_obj)
     if verbose:
         print(f"built {LIB}", file=sys.stderr)
+        print(f"built {MARSHAL}", file=sys.stderr)
     build_ceilings(verbose)
     return LIB
 

@@ -2,6 +2,7 @@
 // Host-side validation of metadata only, then kernel launches on the
 // caller's stream.  See the header for the meaning of every argument.
 #include <math.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -898,6 +899,151 @@ spops_status spops_delta_spmv(int64_t rows, int64_t cols, const int32_t* enc_off
   if (((uintptr_t)enc_values % 16) != 0) return SPOPS_ERR_SHAPE;
   return from_hip(launch_delta_spmv(rows, cols, enc_offsets, codes, enc_values, val_type,
                                     enc_entries, x, y, y_type, as_stream(hip_stream)));
+}
+
+// ----------------------------------------------------- low-rank adapters --
+
+namespace {
+
+constexpr int64_t kLowRankMaxFeatures = (int64_t)1 << 24;
+constexpr int64_t kLowRankMaxTokens = (int64_t)1 << 30;
+
+// Sizes alone.
+spops_status check_low_rank(const spops_low_rank* L) {
+  if (!L) return SPOPS_ERR_NULL;
+  if (!dtype_ok(L->dtype)) return SPOPS_ERR_DTYPE;
+  if (L->tokens < 0 || L->tokens > kLowRankMaxTokens || L->requests < 0 ||
+      L->requests > INT32_MAX - 1 || L->adapters < 1 || L->adapters > 65535 || L->rank < 1 ||
+      L->in_features < 1 || L->in_features > kLowRankMaxFeatures || L->out_features < 1 ||
+      L->out_features > kLowRankMaxFeatures)
+    return SPOPS_ERR_SHAPE;
+  if (L->rank > kLowRankMaxRank) return SPOPS_ERR_UNSUPPORTED;
+  return SPOPS_OK;
+}
+
+// Sizes, leading dimensions, pointers and workspace of a call, and its launch
+// arguments.  `second` is y, dy or null; n_second its rows.
+spops_status low_rank_args(const spops_low_rank* L, int op, const void* second, int64_t lds,
+                           const void* xt, int64_t ldx, void* out, int64_t ldo, void* workspace,
+                           size_t bytes, LowRankArgs& a) {
+  const spops_status st = check_low_rank(L);
+  if (st != SPOPS_OK) return st;
+  if (ldx < L->tokens || ldo < L->tokens) return SPOPS_ERR_SHAPE;
+  if (op != kLowRankProject && lds < L->tokens) return SPOPS_ERR_SHAPE;
+  if (op == kLowRankProject && lds < L->in_features) return SPOPS_ERR_SHAPE;
+  // one launch covers the token tiles times the row blocks
+  const int64_t widest = std::max(L->out_features, L->in_features);
+  if ((L->tokens / 16 + 1) * (widest / 16 + 1) > INT32_MAX) return SPOPS_ERR_SHAPE;
+  if (!L->A || !L->B || (L->requests > 0 && (!L->offsets || !L->adapter))) return SPOPS_ERR_NULL;
+  if (L->tokens > 0) {
+    if (!second || !xt || !out) return SPOPS_ERR_NULL;
+    const LowRankLayout l = lowrank_layout(op, L->dtype, L->tokens, L->requests, L->adapters,
+                                           L->rank, L->in_features, L->out_features);
+    if (!workspace || bytes < l.bytes || ((uintptr_t)workspace & 255)) return SPOPS_ERR_WORKSPACE;
+  }
+  a.T = L->tokens;
+  a.n_in = L->in_features;
+  a.n_out = L->out_features;
+  a.S = (int32_t)L->requests;
+  a.n = (int32_t)L->adapters;
+  a.R = (int32_t)L->rank;
+  a.A = L->A;
+  a.B = L->B;
+  a.offsets = L->offsets;
+  a.adapter = L->adapter;
+  a.ranks = L->ranks;
+  a.scale = L->scale;
+  a.x = xt;
+  a.ldx = ldx;
+  a.out = out;
+  a.ldo = ldo;
+  if (op == kLowRankProject) {
+    a.W = second;
+    a.ldw = lds;
+  } else {
+    a.y = second;
+    a.ldy = lds;
+  }
+  return SPOPS_OK;
+}
+
+}  // namespace
+
+spops_status spops_low_rank_workspace_size(const spops_low_rank* L, spops_low_rank_op op,
+                                           size_t* bytes) {
+  const spops_status st = check_low_rank(L);
+  if (st != SPOPS_OK) return st;
+  if (!bytes) return SPOPS_ERR_NULL;
+  if (op != SPOPS_LOW_RANK_ADD && op != SPOPS_LOW_RANK_PROJECT && op != SPOPS_LOW_RANK_BACKWARD)
+    return SPOPS_ERR_UNSUPPORTED;
+  *bytes = L->tokens == 0 ? 0
+                          : lowrank_layout(op, L->dtype, L->tokens, L->requests, L->adapters,
+                                           L->rank, L->in_features, L->out_features)
+                                .bytes;
+  return SPOPS_OK;
+}
+
+spops_status spops_low_rank_add(const spops_low_rank* L, const void* yt, int64_t ldy,
+                                const void* xt, int64_t ldx, void* out, int64_t ldo,
+                                void* workspace, size_t workspace_bytes, void* hip_stream) {
+  LowRankArgs a{};
+  const spops_status st = low_rank_args(L, kLowRankAdd, yt, ldy, xt, ldx, out, ldo, workspace,
+                                        workspace_bytes, a);
+  if (st != SPOPS_OK || a.T == 0) return st;
+  return from_hip(launch_lowrank(kLowRankAdd, L->dtype, a, workspace, as_stream(hip_stream)));
+}
+
+spops_status spops_low_rank_project(const spops_low_rank* L, const void* W, int64_t ldw,
+                                    const void* xt, int64_t ldx, void* out, int64_t ldo,
+                                    void* workspace, size_t workspace_bytes, void* hip_stream) {
+  LowRankArgs a{};
+  const spops_status st = low_rank_args(L, kLowRankProject, W, ldw, xt, ldx, out, ldo, workspace,
+                                        workspace_bytes, a);
+  if (st != SPOPS_OK || a.T == 0) return st;
+  return from_hip(launch_lowrank(kLowRankProject, L->dtype, a, workspace, as_stream(hip_stream)));
+}
+
+spops_status spops_low_rank_backward(const spops_low_rank* L, const void* dyt, int64_t ldy,
+                                     const void* xt, int64_t ldx, void* dxt, int64_t lddx,
+                                     void* dA, void* dB, void* workspace, size_t workspace_bytes,
+                                     void* hip_stream) {
+  LowRankArgs a{};
+  const spops_status st = low_rank_args(L, kLowRankBackward, dyt, ldy, xt, ldx, dxt, lddx,
+                                        workspace, workspace_bytes, a);
+  if (st != SPOPS_OK) return st;
+  if (!dA || !dB) return SPOPS_ERR_NULL;
+  a.dA = dA;
+  a.dB = dB;
+  return from_hip(launch_lowrank(kLowRankBackward, L->dtype, a, workspace, as_stream(hip_stream)));
+}
+
+// ------------------------------------------- gradient norm and clipping --
+
+spops_status spops_clip_grad_norm_workspace_size(int64_t count, size_t* bytes) {
+  if (!bytes) return SPOPS_ERR_NULL;
+  if (count < 0 || count > (1 << 20)) return SPOPS_ERR_SHAPE;
+  *bytes = clip_workspace_bytes(count);
+  return SPOPS_OK;
+}
+
+spops_status spops_clip_grad_norm(const spops_clip_tensor* tensors, int64_t count,
+                                  double max_norm, float* norm, void* workspace,
+                                  size_t workspace_bytes, void* hip_stream) {
+  static_assert(sizeof(spops_clip_tensor) == sizeof(ClipTensor) &&
+                    offsetof(spops_clip_tensor, dtype) == offsetof(ClipTensor, dtype),
+                "one layout");
+  if (count < 0 || count > (1 << 20)) return SPOPS_ERR_SHAPE;
+  if (!norm || (count > 0 && !tensors)) return SPOPS_ERR_NULL;
+  if (!(max_norm >= 0.0)) return SPOPS_ERR_ARGUMENT;
+  for (int64_t i = 0; i < count; ++i) {
+    if (!dtype_ok(tensors[i].dtype)) return SPOPS_ERR_DTYPE;
+    if (tensors[i].numel < 0 || tensors[i].numel > kClipMaxNumel) return SPOPS_ERR_SHAPE;
+    if (tensors[i].numel > 0 && (!tensors[i].grad || !tensors[i].out)) return SPOPS_ERR_NULL;
+  }
+  if (!workspace || workspace_bytes < clip_workspace_bytes(count) || ((uintptr_t)workspace & 7))
+    return SPOPS_ERR_WORKSPACE;
+  return from_hip(launch_clip((const ClipTensor*)tensors, count, max_norm, norm, workspace,
+                              as_stream(hip_stream)));
 }
 
 }  // extern "C"

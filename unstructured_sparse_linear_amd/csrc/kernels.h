@@ -392,4 +392,54 @@ hipError_t launch_delta_spmv(int64_t m, int64_t n, const int32_t* eo, const uint
                              const void* val, int dtype, int64_t total, const void* x, void* y,
                              int y_dtype, hipStream_t s);
 
+// ------------------------------------------------- low-rank adapters --
+enum LowRankOp : int { kLowRankAdd = 0, kLowRankProject = 1, kLowRankBackward = 2 };
+constexpr int64_t kLowRankMaxRank = 256;
+struct LowRankArgs {
+  int64_t T, n_in, n_out;  // tokens, features in and out
+  int64_t ldx, ldy, ldo, ldw;
+  int32_t S, n, R;         // requests, adapters in the pool, stacked rank
+  const void* x;           // [n_in][T]
+  const void* y;           // add: base y; backward: dy  [n_out][T]
+  const void* A;           // [n][R][n_in]
+  const void* B;           // [n][n_out][R]
+  const void* W;           // project: [n_out][n_in]
+  void* out;               // add, project: [n_out][T]; backward: dx [n_in][T]
+  void* dA;
+  void* dB;
+  const int32_t* offsets;  // [S+1]
+  const int32_t* adapter;  // [S]
+  const int32_t* ranks;    // [n] or null (R)
+  const float* scale;      // [n] or null (1)
+  // filled from the workspace by launch_lowrank
+  int64_t Tp;              // row length of u and du
+  int32_t* tokad;          // [Tp] adapter of each token, -1 for none
+  float* u;                // [slices_u][R][Tp]
+  float* du;
+  void* packed;            // project: x as MFMA fragments
+};
+// How a call is cut, and where its workspace parts lie.
+struct LowRankLayout {
+  int64_t Tp;
+  int width;               // tokens a lane holds of a row (tile: 16 width)
+  int groups;              // workgroups that share a tile's adapters
+  int slices_u, slices_du; // slices of the features
+  size_t at_tokad, at_u, at_du, at_packed, bytes;
+};
+LowRankLayout lowrank_layout(int op, int dtype, int64_t T, int64_t S, int64_t n, int64_t R,
+                             int64_t n_in, int64_t n_out);
+hipError_t launch_lowrank(int op, int dtype, LowRankArgs a, void* ws, hipStream_t s);
+
+// -------------------------------------------- gradient norm and clipping --
+struct ClipTensor {
+  const void* grad;
+  void* out;
+  int64_t numel;
+  int32_t dtype;
+};
+constexpr int64_t kClipMaxNumel = (int64_t)1 << 36;
+size_t clip_workspace_bytes(int64_t count);
+hipError_t launch_clip(const ClipTensor* t, int64_t count, double max_norm, float* norm, void* ws,
+                       hipStream_t s);
+
 }  // namespace spops

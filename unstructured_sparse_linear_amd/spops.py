@@ -1,4 +1,5 @@
-"""Python binding of libspops (ctypes).  Argument marshalling only: every step
+"""Python binding of libspops (ctypes; the low-rank adapter and clipping calls go
+through the compiled _marshal.so).  Argument marshalling only: every step
 of every operation runs in the HIP kernels behind the C ABI in
 include/spops.h; PyTorch provides device memory and the current stream.
 
@@ -13,7 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 from collections import OrderedDict
-from typing import Optional, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 
@@ -50,6 +51,22 @@ class CSRDesc(ctypes.Structure):
                 ("row_idx_type", ctypes.c_int), ("values", ctypes.c_void_p),
                 ("row_offsets", ctypes.c_void_p), ("row_idx", ctypes.c_void_p),
                 ("col_idx", ctypes.c_void_p)]
+
+
+class LowRankDesc(ctypes.Structure):
+    """spops_low_rank of include/spops.h."""
+    _fields_ = [("tokens", ctypes.c_int64), ("requests", ctypes.c_int64),
+                ("adapters", ctypes.c_int64), ("rank", ctypes.c_int64),
+                ("in_features", ctypes.c_int64), ("out_features", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("adapter", ctypes.c_void_p),
+                ("ranks", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class ClipTensor(ctypes.Structure):
+    """spops_clip_tensor of include/spops.h."""
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
 
 
 _lib = None
@@ -104,6 +121,14 @@ def lib() -> ctypes.CDLL:
                                   i32),
             "spops_cg": ([cp, vp, vp, ctypes.c_double, i64, i64, vp, vp, sz, P(i64),
                           P(ctypes.c_double), vp], i32),
+            "spops_low_rank_workspace_size": ([P(LowRankDesc), i32, P(sz)], i32),
+            "spops_low_rank_add": ([P(LowRankDesc), vp, i64, vp, i64, vp, i64, vp, sz, vp], i32),
+            "spops_low_rank_project": ([P(LowRankDesc), vp, i64, vp, i64, vp, i64, vp, sz, vp],
+                                       i32),
+            "spops_low_rank_backward": ([P(LowRankDesc), vp, i64, vp, i64, vp, i64, vp, vp, vp,
+                                         sz, vp], i32),
+            "spops_clip_grad_norm_workspace_size": ([i64, P(sz)], i32),
+            "spops_clip_grad_norm": ([P(ClipTensor), i64, ctypes.c_double, vp, vp, sz, vp], i32),
         }
         for name, (args, res) in sigs.items():
             f = getattr(L, name)
@@ -111,6 +136,24 @@ def lib() -> ctypes.CDLL:
             f.restype = res
         _lib = L
     return _lib
+
+
+_marshal_module = None
+
+
+def _marshal():
+    """The compiled part of the binding (_marshal.so, built with libspops.so);
+    raises if either is missing."""
+    global _marshal_module
+    if _marshal_module is None:
+        lib()
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise RuntimeError("_marshal.so is missing or was built for another torch; build it "
+                               "with `python -m unstructured_sparse_linear_amd.build`") from e
+        _marshal_module = m
+    return _marshal_module
 
 
 def _check(fn: str, code: int):
@@ -623,6 +666,59 @@ def masked_adam(values: torch.Tensor, grad: torch.Tensor, exp_avg: torch.Tensor,
         _ptr(exp_avg), _ptr(exp_avg_sq), int(step), float(lr), float(betas[0]),
         float(betas[1]), float(eps), int(bool(maximize)), _stream(values)))
     return values
+
+
+def low_rank_add(yt: torch.Tensor, xt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                 offsets: torch.Tensor, adapter: torch.Tensor,
+                 scale: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """yt + the low-rank adapters of many requests, applied to xt.
+
+    Request i owns the tokens [offsets[i], offsets[i+1]) and the adapter
+    a = adapter[i] of the pool; on its tokens y += scale[a] B[a] A[a] x, with
+    the first ranks[a] ranks (all of them without `ranks`).  Tokens outside
+    every request and requests with an adapter outside the pool (-1) keep yt.
+
+      yt [out_features, tokens], xt [in_features, tokens]: rows of unit stride
+      A [adapters, rank, in_features], B [adapters, out_features, rank]
+      offsets [requests + 1], adapter [requests], ranks [adapters]: int32
+      scale [adapters]: float32
+
+    All matrices share a dtype (f32, f16, bf16); sums are fp32, one rounding.
+    `out` may be yt.  Not differentiable by itself: see LowRankAdapters."""
+    return _marshal().low_rank_add(yt, xt, A, B, offsets, adapter, scale, ranks, out)
+
+
+def low_rank_project(W: torch.Tensor, xt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                     offsets: torch.Tensor, adapter: torch.Tensor,
+                     scale: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """W xt + the requests' adapters in one pass over W (low_rank_add has the
+    other arguments): for the few tokens of a decode step.  Correct for any
+    number of tokens; for prompts a dense product and low_rank_add are
+    faster."""
+    return _marshal().low_rank_project(W, xt, A, B, offsets, adapter, scale, ranks, out)
+
+
+def low_rank_backward(dyt: torch.Tensor, xt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                      offsets: torch.Tensor, adapter: torch.Tensor,
+                      scale: Optional[torch.Tensor] = None,
+                      ranks: Optional[torch.Tensor] = None
+                      ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients (dxt, dA, dB) of low_rank_add's adapters for dyt = dL/dyt.
+    dxt is the adapters' part alone (zero on tokens without one); the base
+    passes dyt through.  dA and dB are zero for unused adapters and past an
+    adapter's rank.  Deterministic: no atomics."""
+    return _marshal().low_rank_backward(dyt, xt, A, B, offsets, adapter, scale, ranks)
+
+
+def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float,
+                   out: Optional[Sequence[torch.Tensor]] = None) -> torch.Tensor:
+    """Scales the gradients by min(1, max_norm / (norm + 1e-6)), with norm the
+    2-norm over all of them, in place or into the tensors `out`; returns the
+    norm (float32, on the device: nothing synchronizes).  Any mix of f32, f16
+    and bf16 tensors.  A NaN norm makes every value NaN."""
+    return _marshal().clip_grad_norm(grads, max_norm, out)
 
 
 class DeltaMatrix:
