@@ -934,6 +934,11 @@ spops_status low_rank_args(const spops_low_rank* L, int op, const void* second, 
   // one launch covers the token tiles times the row blocks
   const int64_t widest = std::max(L->out_features, L->in_features);
   if ((L->tokens / 16 + 1) * (widest / 16 + 1) > INT32_MAX) return SPOPS_ERR_SHAPE;
+  // and the gradients' the factors' rows
+  if (op == kLowRankBackward &&
+      ((L->in_features + L->out_features) / 32 + 2) * L->adapters * ((L->rank + 63) / 64) +
+              (L->tokens / 64 + 1) * (widest / 64 + 1) > INT32_MAX)
+    return SPOPS_ERR_SHAPE;
   if (!L->A || !L->B || (L->requests > 0 && (!L->offsets || !L->adapter))) return SPOPS_ERR_NULL;
   if (L->tokens > 0) {
     if (!second || !xt || !out) return SPOPS_ERR_NULL;

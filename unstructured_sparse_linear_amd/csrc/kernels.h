@@ -417,6 +417,12 @@ struct LowRankArgs {
   float* u;                // [slices_u][R][Tp]
   float* du;
   void* packed;            // project: x as MFMA fragments
+  void* rows;              // [Tp] packed ranks of u (add) or du (backward)
+  float* up;               // [Tp] their scales (f16)
+  void* ru;                // backward: halves of u and du, [2][R][Tp] (f32: [R][Tp])
+  void* rdu;
+  uint8_t* eu;             // backward: their scales' exponents (f16), [R][Tp]
+  uint8_t* edu;
 };
 // How a call is cut, and where its workspace parts lie.
 struct LowRankLayout {
@@ -424,7 +430,7 @@ struct LowRankLayout {
   int width;               // tokens a lane holds of a row (tile: 16 width)
   int groups;              // workgroups that share a tile's adapters
   int slices_u, slices_du; // slices of the features
-  size_t at_tokad, at_u, at_du, at_packed, bytes;
+  size_t at_tokad, at_u, at_du, at_packed, at_rows, at_up, at_ru, at_rdu, at_eu, at_edu, bytes;
 };
 LowRankLayout lowrank_layout(int op, int dtype, int64_t T, int64_t S, int64_t n, int64_t R,
                              int64_t n_in, int64_t n_out);

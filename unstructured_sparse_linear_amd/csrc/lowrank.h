@@ -187,6 +187,16 @@ __device__ __forceinline__ void store_bits(_Float16* p, uint32_t b) {
 }
 __device__ __forceinline__ void store_bits(bf16_t* p, uint32_t b) { p->bits = (uint16_t)b; }
 
+// Element e of a row as fp32.
+template <typename T, int V>
+__device__ __forceinline__ float row_f32(const Row<T, V>& r, int e) {
+  const uint32_t b = r.w[e * sizeof(T) / 4];
+  if constexpr (sizeof(T) == 4)
+    return __uint_as_float(b);
+  else
+    return e % 2 ? hi_f32(b, (T*)nullptr) : lo_f32(b, (T*)nullptr);
+}
+
 // C consecutive elements as fp32, and back; the first `cnt` only where the
 // row ends inside.
 template <typename T, int C>

@@ -18,10 +18,11 @@
 //
 // Kernels:
 //   shrink   u (and du) as fp32 partial sums over slices of the features
-//   join     adds the slices (backward, where u is read many times)
+//   pack     adds the slices and splits them into operands, where they are
+//            read many times
 //   expand   y + B u
-//   dx       A^T du
-//   outer    dA and dB, one workgroup per adapter and 64 features
+//   gradients  dA and dB, one workgroup per adapter and 32 features, and
+//            dx = A^T du
 //   project  W x + B u on few tokens
 // Requests meet the tiles only through each token's adapter, which the shrink
 // kernel finds and writes once.  A tile whose tokens have several adapters is
@@ -33,10 +34,15 @@
 namespace spops {
 namespace {
 
-constexpr int kThreads = 256;       // shrink, expand, dx, join: four waves
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
+constexpr int kThreads = 256;       // four waves
 constexpr int kWaves = kThreads / kWave;
-constexpr int kOuterThreads = 512;  // outer, project: eight waves
-constexpr int kOuterWaves = kOuterThreads / kWave;
+constexpr int kProjectThreads = 512;  // project: eight waves
+constexpr int kProjectWaves = kProjectThreads / kWave;
 
 // ------------------------------------------------------ adapters of tokens --
 
@@ -312,18 +318,106 @@ __global__ __launch_bounds__(kThreads) void lowrank_shrink_kernel(LowRankArgs a,
     shrink_tile<T, V, NR, true, false>(a, jy, blockIdx.z - jx.slices, groups, red, tile);
 }
 
-// ------------------------------------------------------------------- join --
+// ------------------------------------------------------------------- pack --
 
-// Adds the slices of u and du into slice 0, in order.
-__global__ __launch_bounds__(kThreads) void lowrank_join_kernel(LowRankArgs a, int su, int sd) {
-  float* u = blockIdx.y ? a.du : a.u;
-  const int slices = blockIdx.y ? sd : su;
-  const int64_t size = (int64_t)a.R * a.Tp;
-  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;  // Tp is a multiple of 32
-  if (i >= size) return;
-  f32x4 v = *(const f32x4*)(u + i);
-  for (int s = 1; s < slices; ++s) v += *(const f32x4*)(u + s * size + i);
-  *(f32x4*)(u + i) = v;
+// Bytes of a token's packed ranks: 64 for ranks up to 16, else 128 per 32
+// ranks (hi and lo of a 16-bit type, or fp32).
+__host__ __device__ inline int packed_row(int R) { return R <= 16 ? 64 : (R + 31) / 32 * 128; }
+
+constexpr int kPackTokens = 64;
+
+// Adds the slices of u (or du) in order and writes them as the operands that
+// the later kernels load, so that the sum and the split into halves are made
+// once and not by every workgroup that reads them:
+//   rows   [token][ranks], for expand (u) and dx (du); f16: scaled by token
+//   ru, rdu  [hi, lo][rank][token], for outer; f16: scaled by rank over the
+//          tokens of one adapter in a block of 32, the exponent kept beside
+template <typename T, bool BACKWARD>
+__global__ __launch_bounds__(kThreads) void lowrank_pack_kernel(LowRankArgs a, int su, int sd) {
+  constexpr int TT = kPackTokens, LD = TT + 1;
+  extern __shared__ float us[];
+  __shared__ float down[TT];
+  const bool is_du = BACKWARD && blockIdx.y == 1;
+  const float* u = is_du ? a.du : a.u;
+  const int slices = is_du ? sd : su, tid = threadIdx.x, R = a.R;
+  const int64_t t0 = (int64_t)blockIdx.x * TT, size = (int64_t)R * a.Tp;
+  for (int i = tid; i < R * (TT / 4); i += kThreads) {
+    const int r = i / (TT / 4), t = i % (TT / 4) * 4;
+    const float* p = u + (int64_t)r * a.Tp + t0 + t;
+    f32x4 v = *(const f32x4*)p;
+#pragma unroll 4
+    for (int s = 1; s < slices; ++s) v += *(const f32x4*)(p + s * size);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) us[r * LD + t + e] = v[e];
+  }
+  __syncthreads();
+  if (!BACKWARD || is_du) {
+    if constexpr (__is_same(T, _Float16)) {
+      if (tid < TT) {
+        float m = 0.f;
+        for (int r = 0; r < R; ++r) m = fmaxf(m, fabsf(us[r * LD + tid]));
+        const Pow2 p = pow2_of(m);
+        down[tid] = p.down;
+        a.up[t0 + tid] = p.up;
+      }
+      __syncthreads();
+    }
+    const int pieces = packed_row(R) / 16;
+    for (int i = tid; i < TT * pieces; i += kThreads) {
+      const int t = i / pieces, c = i % pieces;
+      uint32_t w[4];
+      if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = c * 4 + e < R ? __float_as_uint(us[(c * 4 + e) * LD + t]) : 0u;
+      } else {
+        const bool lo = R <= 16 ? c >= 2 : c % 8 >= 4;
+        const int r = R <= 16 ? c % 2 * 8 : c / 8 * 32 + c % 4 * 8;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[e] = r + e < R ? us[(r + e) * LD + t] : 0.f;
+          if constexpr (__is_same(T, _Float16)) v[e] *= down[t];
+        }
+        const Frag<T> f = split8<T>(v, lo);
+        __builtin_memcpy(w, &f, 16);
+      }
+      __builtin_memcpy(__builtin_assume_aligned((char*)a.rows + (t0 + t) * (pieces * 16) + c * 16, 16),
+                       w, 16);
+    }
+  }
+  if constexpr (BACKWARD) {
+    const int lane = tid % kWave;
+    const int64_t t = t0 + lane;
+    const int ad = __is_same(T, _Float16) && t < a.T ? a.tokad[t] : -1;
+    for (int r = tid / kWave; r < R; r += kWaves) {
+      float v = us[r * LD + lane];
+      const int64_t at = (int64_t)r * a.Tp + t;
+      if constexpr (sizeof(T) == 4) {
+        ((float*)(is_du ? a.rdu : a.ru))[at] = v;
+      } else {
+        if constexpr (__is_same(T, _Float16)) {
+          float big = 0.f;
+          uint64_t rest = __ballot(ad >= 0);
+          while (rest) {
+            const int l = __builtin_ctzll(rest);
+            const bool same = ad == __builtin_amdgcn_readlane(ad, l) && lane / 32 == l / 32;
+            float m = same ? fabsf(v) : 0.f;
+#pragma unroll
+            for (int o = 1; o < kWave; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
+            big = same ? m : big;
+            rest &= ~__ballot(same);
+          }
+          const Pow2 p = pow2_of(big);
+          v *= p.down;
+          (is_du ? a.edu : a.eu)[at] = (uint8_t)(__float_as_uint(p.up) >> 23);
+        }
+        T* out = (T*)(is_du ? a.rdu : a.ru) + at;
+        store_bits(out, split_bits(v, false, (T*)nullptr));
+        store_bits(out + size, split_bits(v, true, (T*)nullptr));
+      }
+    }
+  }
 }
 
 // --------------------------------------------- u as an operand, from shared --
@@ -387,21 +481,31 @@ __device__ __forceinline__ Frag<T> u_frag(const float* row, int step, bool lo, f
   return split8<T>(v, lo);
 }
 
-// c + u F^T for one K block, F's fragment laid out the same way.
+// c + F u for one K block: result rows are F's, columns are u's tokens.
 template <typename T, bool SMALL>
-__device__ __forceinline__ f32x4 u_mma(const Frag<T>& hi, const Frag<T>& lo, const Frag<T>& f,
+__device__ __forceinline__ f32x4 u_mma(const Frag<T>& f, const Frag<T>& hi, const Frag<T>& lo,
                                        f32x4 c) {
   if constexpr (SMALL && sizeof(T) == 4) {
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(hi.w[s]), __uint_as_float(f.w[s]),
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(f.w[s]), __uint_as_float(hi.w[s]),
                                                c, 0, 0, 0);
     return c;
   } else {
-    c = mma(hi, f, c);
-    if constexpr (!SMALL && sizeof(T) == 2) c = mma(lo, f, c);
+    c = mma(f, hi, c);
+    if constexpr (!SMALL && sizeof(T) == 2) c = mma(f, lo, c);
     return c;
   }
+}
+
+// The same turned: rows are u's tokens.
+template <typename T, bool SMALL>
+__device__ __forceinline__ f32x4 token_mma(const Frag<T>& hi, const Frag<T>& lo, const Frag<T>& f,
+                                           f32x4 c) {
+  if constexpr (SMALL && sizeof(T) == 4) return u_mma<T, true>(hi, f, f, c);
+  c = mma(hi, f, c);
+  if constexpr (!SMALL && sizeof(T) == 2) c = mma(lo, f, c);
+  return c;
 }
 
 // Fragment of B_ad's row o: ranks from rank_base, zero from the adapter's rank
@@ -421,306 +525,425 @@ __device__ __forceinline__ Frag<T> b_frag(const LowRankArgs& a, int ad, int64_t 
   return f;
 }
 
-// Token order of the streaming kernels: result row m of product q stands for
-// this token of the tile, so that a lane's rows over q are runs of eight
-// (Q >= 2) or four tokens in memory.
-template <int Q>
-__device__ __forceinline__ int tile_token(int q, int m) {
-  return Q == 1 ? m : (q / 2) * 32 + (m / 4) * 8 + (q % 2) * 4 + m % 4;
-}
-
-// The tile's u rows as operands: kept in registers for up to STEPS K blocks,
-// read from shared memory again where there are more.
-template <typename T, int Q, int STEPS, bool SMALL>
-struct UOperand {
-  Frag<T> hi[Q][STEPS > 0 ? STEPS : 1], lo[Q][STEPS > 0 ? STEPS : 1];
-  float down[Q];
-  f32x4 up[Q];
-  const float* row[Q];
-  int blocks;
-  __device__ __forceinline__ UOperand(const LowRankArgs& a, const float* us) {
-    const int m = lane_id() % 16, g = lane_id() / 16;
-    blocks = SMALL ? 1 : (a.R + 31) / 32;
+// Fragment of feature f of A_ad, likewise (A's rows run along the features).
+template <typename T, bool SMALL>
+__device__ __forceinline__ Frag<T> at_frag(const LowRankArgs& a, int ad, int64_t f, int rank,
+                                           int step) {
+  constexpr int W = SMALL && sizeof(T) == 4 ? 4 : 8;
+  const int r = rank_base<T, SMALL>(step);
+  const T* p = (const T*)a.A + (int64_t)ad * a.R * a.n_in + f;
+  uint32_t b[8];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      row[q] = us + tile_token<Q>(q, m) * staged_width(a.R);
-      const Pow2 p = row_pow2<T>(row[q], a.R);
-      down[q] = p.down;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        up[q][i] = __is_same(T, _Float16) ? __shfl(p.up, g * 4 + i, kWave) : 1.f;
-#pragma unroll
-      for (int k = 0; k < STEPS; ++k) {
-        hi[q][k] = u_frag<T, SMALL>(row[q], k, false, down[q]);
-        if constexpr (!SMALL && sizeof(T) == 2) lo[q][k] = u_frag<T, SMALL>(row[q], k, true, down[q]);
-      }
+  for (int s = 0; s < 8; ++s) {
+    b[s] = 0u;
+    if (s < W) {
+      const uint32_t v = raw_bits(p + (int64_t)(r + s < a.R ? r + s : a.R - 1) * a.n_in);
+      b[s] = r + s < rank ? v : 0u;
     }
   }
-  // acc[q] += u_q F^T for block k (not yet scaled by up)
-  __device__ __forceinline__ void product(int k, const Frag<T>& f, f32x4 (&acc)[Q]) const {
+  Frag<T> out;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
+  for (int s = 0; s < 8; ++s) {
+    if (sizeof(T) == 4)
+      out.w[s] = b[s];
+    else if (s % 2 == 0)
+      out.w[s / 2] = b[s] | b[s + 1] << 16;
+  }
+  return out;
+}
+
+// The adapters of a tile of tokens: each token's own, and the distinct ones
+// with their ranks, in order of their first token.
+template <int TT>
+struct TileAdapters {
+  int tok[TT];
+  int ad[TT];
+  int rank[TT];
+  int count;
+};
+
+template <int TT, int THREADS>
+__device__ __forceinline__ void load_tokad(const LowRankArgs& a, int64_t t0, int* tok) {
+  for (int t = threadIdx.x; t < TT; t += THREADS) {
+    const int ad = t0 + t < a.T ? a.tokad[t0 + t] : -1;
+    tok[t] = ad < a.n ? ad : -1;
+  }
+}
+
+// By all threads; ends with a barrier.
+template <int TT, int THREADS>
+__device__ __forceinline__ void tile_adapters(const LowRankArgs& a, int64_t t0,
+                                              TileAdapters<TT>& s) {
+  load_tokad<TT, THREADS>(a, t0, s.tok);
+  __syncthreads();
+  if (threadIdx.x < kWave) {
+    AdapterWalk<TT> walk(s.tok);
+    int ad, c = 0, mine0 = -1, mine1 = -1;
+    while (walk.next(ad)) {
+      if (c % kWave == lane_id()) (c < kWave ? mine0 : mine1) = ad;
+      ++c;
+    }
+    const int l = lane_id();
+    if (l < c) {
+      s.ad[l] = mine0;
+      s.rank[l] = rank_of(a, mine0);
+    }
+    if (TT > kWave && l + kWave < c) {
+      s.ad[l + kWave] = mine1;
+      s.rank[l + kWave] = rank_of(a, mine1);
+    }
+    if (l == 0) s.count = c;
+  }
+  __syncthreads();
+}
+
+// The tile's ranks as operands.  Column n of product q is the token V n + q,
+// so that a lane's V columns are neighbours in memory.  They come packed from
+// memory (PACKED) or from the fp32 rows staged in shared memory, and stay in
+// registers for up to STEPS K blocks (packed ones are loaded again where there
+// are more).
+template <typename T, int V, int STEPS, bool SMALL, bool PACKED>
+struct UOperand {
+  static constexpr int N = STEPS > 0 ? STEPS : 1;
+  Frag<T> hi[V][N], lo[V][N];
+  float up[V], down[V];
+  const char* row;
+  const float* us;
+  int row_bytes, width, blocks;
+
+  __device__ __forceinline__ void get(int q, int k, Frag<T>& h, Frag<T>& l) const {
+    const int g = lane_id() / 16;
+    if constexpr (PACKED) {
+      const char* p = row + q * row_bytes;
+      if constexpr (SMALL)
+        __builtin_memcpy(&h, __builtin_assume_aligned(p + g * 16, 16), 16);
+      else if constexpr (sizeof(T) == 4)
+        __builtin_memcpy(&h, __builtin_assume_aligned(p + k * 128 + g * 32, 16), 32);
+      else {
+        __builtin_memcpy(&h, __builtin_assume_aligned(p + k * 128 + g * 16, 16), 16);
+        __builtin_memcpy(&l, __builtin_assume_aligned(p + k * 128 + 64 + g * 16, 16), 16);
+      }
+    } else {
+      h = u_frag<T, SMALL>(us + q * width, k, false, down[q]);
+      if constexpr (!SMALL && sizeof(T) == 2) l = u_frag<T, SMALL>(us + q * width, k, true, down[q]);
+    }
+  }
+  __device__ __forceinline__ UOperand(const LowRankArgs& a, int64_t t0, const float* staged) {
+    const int n = lane_id() % 16;
+    blocks = SMALL ? 1 : (a.R + 31) / 32;
+    row_bytes = packed_row(a.R);
+    width = staged_width(a.R);
+    row = (const char*)a.rows + (t0 + n * V) * row_bytes;
+    us = staged + n * V * width;
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      up[q] = down[q] = 1.f;
+      if constexpr (__is_same(T, _Float16)) {
+        if constexpr (PACKED) {
+          up[q] = a.up[t0 + n * V + q];
+        } else {
+          const Pow2 p = row_pow2<T>(us + q * width, a.R);
+          up[q] = p.up;
+          down[q] = p.down;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < STEPS; ++k) get(q, k, hi[q][k], lo[q][k]);
+    }
+  }
+  // acc[q] += f u_q for block k (not yet scaled by up)
+  __device__ __forceinline__ void product(int k, const Frag<T>& f, f32x4 (&acc)[V]) const {
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
       if constexpr (STEPS > 0) {
-        acc[q] = u_mma<T, SMALL>(hi[q][k], lo[q][k], f, acc[q]);
+        acc[q] = u_mma<T, SMALL>(f, hi[q][k], lo[q][k], acc[q]);
       } else {
-        const Frag<T> h = u_frag<T, SMALL>(row[q], k, false, down[q]);
-        const Frag<T> l = sizeof(T) == 2 ? u_frag<T, SMALL>(row[q], k, true, down[q]) : h;
-        acc[q] = u_mma<T, SMALL>(h, l, f, acc[q]);
+        Frag<T> h, l;
+        get(q, k, h, l);
+        acc[q] = u_mma<T, SMALL>(f, h, l, acc[q]);
       }
     }
   }
 };
 
-// Adapters of the result rows a lane holds.
-template <int Q>
-__device__ __forceinline__ void row_adapters(const int* tok, int (&ra)[Q][4]) {
-  const int g = lane_id() / 16;
+// --------------------------------------------------------- expand and dx --
+
+// Rows ob + 4 (lane / 16) + i of a matrix, V tokens from `t` a lane.
+template <typename T, int V>
+__device__ __forceinline__ void load_rows(const T* p, int64_t ld, int64_t ob, int64_t rows,
+                                          int64_t t, int cnt, Row<T, V> (&y)[4]) {
 #pragma unroll
-  for (int q = 0; q < Q; ++q)
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = ob + lane_id() / 16 * 4 + i;
+    const T* at = p + (r < rows ? r : rows - 1) * ld + t;
+    if (cnt >= V) {
+      y[i] = load_row<T, V>(at);
+    } else {
+      zero_row(y[i]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ra[q][i] = tok[tile_token<Q>(q, g * 4 + i)];
+      for (int e = 0; e < V; ++e)
+        if (e < cnt) y[i].w[e * sizeof(T) / 4] |= raw_bits(at + e) << (e * sizeof(T) * 8 % 32);
+    }
+  }
 }
 
-template <int TT, int THREADS>
-__device__ __forceinline__ void load_tokad(const LowRankArgs& a, int64_t t0, int* tok) {
-  for (int t = threadIdx.x; t < TT; t += THREADS) tok[t] = t0 + t < a.T ? a.tokad[t0 + t] : -1;
+// expand: out = y + B u (out may be y itself).  DX: out = A^T du, zero where a
+// token has no adapter.  A workgroup keeps the ranks of 16 V tokens in
+// registers and walks rows of the output, 16 a wave at a time: sixteen lanes
+// hold 16 V neighbouring tokens of a row (256 bytes), four rows a load.  The
+// next rows' values and factors are requested before the present ones are
+// used.  Distinct adapters are computed for the whole tile one after another
+// (D at a time in flight) and selected per token.
+template <typename T, int V, int STEPS, bool SMALL, bool PACKED, bool DX>
+__device__ __forceinline__ void stream_rows(const LowRankArgs& a, const TileAdapters<16 * V>& tile,
+                                            const float* staged, int64_t t0, int64_t row0,
+                                            int64_t row_end) {
+  constexpr int D = V == 1 ? 4 : 1, N = STEPS > 0 ? STEPS : 1;
+  const int lane = lane_id(), n = lane % 16, wave = threadIdx.x / kWave;
+  const UOperand<T, V, STEPS, SMALL, PACKED> u(a, t0, staged);
+  const int64_t rows = DX ? a.n_in : a.n_out, t = t0 + n * V;
+  const int cnt = clampi(a.T - t, 0, V);
+  const int count = __builtin_amdgcn_readfirstlane(tile.count);
+  int ra[V];
+#pragma unroll
+  for (int q = 0; q < V; ++q) ra[q] = tile.tok[n * V + q];
+  const T* y = (const T*)a.y;
+  T* out = (T*)a.out;
+  auto factor = [&](int c, int64_t ob, int k) {
+    const int at = c < count ? c : count - 1;
+    const int ad = __builtin_amdgcn_readfirstlane(tile.ad[at]);
+    const int rank = __builtin_amdgcn_readfirstlane(tile.rank[at]);
+    const int64_t r = ob + n < rows ? ob + n : rows - 1;
+    if constexpr (DX)
+      return at_frag<T, SMALL>(a, ad, r, rank, k);
+    else
+      return b_frag<T, SMALL>(a, ad, r, rank, k);
+  };
+  Row<T, V> yv[4], yn[4];
+  Frag<T> f[D][N], fn[D][N];
+  int64_t ob = row0 + wave * 16;
+  if (ob >= row_end) return;
+  if constexpr (!DX) load_rows<T, V>(y, a.ldy, ob, rows, t, cnt, yn);
+  if (STEPS > 0 && count > 0) {
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int k = 0; k < N; ++k) fn[d][k] = factor(d, ob, k);
+  }
+  for (; ob < row_end; ob += kWaves * 16) {
+    const int64_t next = ob + kWaves * 16 < row_end ? ob + kWaves * 16 : ob;
+    float v[4][V];
+    if constexpr (!DX) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) yv[i] = yn[i];
+      load_rows<T, V>(y, a.ldy, next, rows, t, cnt, yn);
+    }
+    if (STEPS > 0 && count > 0) {
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          f[d][k] = fn[d][k];
+          fn[d][k] = factor(d, next, k);
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < V; ++q) v[i][q] = DX ? 0.f : row_f32<T, V>(yv[i], q);
+    for (int c0 = 0; c0 < count; c0 += D) {
+      if (STEPS > 0 && c0 > 0) {
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+#pragma unroll
+          for (int k = 0; k < N; ++k) f[d][k] = factor(c0 + d, ob, k);
+      }
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (d > 0 && c0 + d >= count) break;
+        const int ad = __builtin_amdgcn_readfirstlane(tile.ad[c0 + d]);
+        f32x4 acc[V];
+#pragma unroll
+        for (int q = 0; q < V; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (STEPS > 0) {
+#pragma unroll
+          for (int k = 0; k < STEPS; ++k) u.product(k, f[d][k], acc);
+        } else {
+          for (int k = 0; k < u.blocks; ++k) u.product(k, factor(c0 + d, ob, k), acc);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int q = 0; q < V; ++q) {
+            const float w = __is_same(T, _Float16) ? acc[q][i] * u.up[q] : acc[q][i];
+            v[i][q] = ra[q] != ad ? v[i][q] : DX ? w : v[i][q] + w;
+          }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = ob + lane / 16 * 4 + i;
+      if (r < rows) store_chunk<T, V>(out + r * a.ldo + t, cnt, v[i]);
+    }
+  }
 }
 
-// ----------------------------------------------------------------- expand --
-
-// out = y + B u.  A wave takes 16 output rows at a time: y's values go through
-// registers in the products' own layout, eight tokens (16 bytes in f16) a
-// lane, and are stored once.  out may be y itself.
-template <typename T, int Q, int STEPS, bool SMALL>
+// Token tiles are the fastest index, so that neighbouring workgroups stream
+// neighbouring parts of the same rows.
+template <typename T, int V, int STEPS, bool SMALL>
 __global__ __launch_bounds__(kThreads) void lowrank_expand_kernel(LowRankArgs a, int slices,
-                                                                  int rows_per_block,
-                                                                  int row_blocks) {
-  constexpr int TT = 16 * Q, C = Q == 1 ? 4 : 8, P = TT / (4 * C);
+                                                                  int tiles, int rows_per_block) {
+  constexpr int TT = 16 * V;
   extern __shared__ float us[];
-  __shared__ int tok[TT];
-  const int lane = lane_id(), n = lane % 16, g = lane / 16, wave = threadIdx.x / kWave;
-  const int block = blockIdx.x % row_blocks;
-  const int64_t t0 = (int64_t)(blockIdx.x / row_blocks) * TT;
-  load_tokad<TT, kThreads>(a, t0, tok);
-  stage_u<TT, kThreads>(a, a.u, slices, t0, us);
-  __syncthreads();
-  const UOperand<T, Q, STEPS, SMALL> u(a, us);
-  int ra[Q][4];
-  row_adapters<Q>(tok, ra);
-  const int64_t o_end0 = (int64_t)(block + 1) * rows_per_block;
-  const int64_t o_end = o_end0 < a.n_out ? o_end0 : a.n_out;
-  const int64_t left = a.T - t0;
-  const T* y = (const T*)a.y + t0;
-  T* out = (T*)a.out + t0;
-  for (int64_t ob = (int64_t)block * rows_per_block + wave * 16; ob < o_end;
-       ob += kWaves * 16) {
-    const int64_t o = ob + n < a.n_out ? ob + n : a.n_out - 1;
-    float v[P][C];
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int t = p * 4 * C + g * C;
-      load_chunk<T, C>(y + o * a.ldy + t, clampi(left - t, 0, C), v[p]);
-    }
-    AdapterWalk<TT> walk(tok);
-    int ad;
-    while (walk.next(ad)) {
-      const int rank = rank_of(a, ad);
-      f32x4 acc[Q];
-#pragma unroll
-      for (int q = 0; q < Q; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const int blocks = STEPS > 0 ? STEPS : u.blocks;
-      for (int k = 0; k < blocks; ++k) u.product(k, b_frag<T, SMALL>(a, ad, o, rank, k), acc);
-#pragma unroll
-      for (int q = 0; q < Q; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float& d = v[q * 4 / C][(q * 4) % C + i];
-          d = ra[q][i] == ad ? d + acc[q][i] * u.up[q][i] : d;
-        }
-    }
-    if (ob + n < a.n_out) {
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int t = p * 4 * C + g * C;
-        store_chunk<T, C>(out + o * a.ldo + t, clampi(left - t, 0, C), v[p]);
-      }
-    }
-  }
-}
-
-// --------------------------------------------------------------------- dx --
-
-// dx = A^T du, zero where a token has no adapter.  A's rows run along the
-// features: eight ranks of V features a lane are turned as x is in shrink, and
-// product j gives the features f0 + V n + j.
-template <typename T, int Q, int V, int STEPS, bool SMALL>
-__global__ __launch_bounds__(kThreads) void lowrank_dx_kernel(LowRankArgs a, int slices,
-                                                              int rows_per_block, int row_blocks) {
-  constexpr int TT = 16 * Q, C = Q == 1 ? 4 : 8, P = TT / (4 * C);
-  constexpr int KR = SMALL && sizeof(T) == 4 ? 4 : 8;  // ranks a lane holds of a block
-  extern __shared__ float us[];
-  __shared__ int tok[TT];
-  const int lane = lane_id(), n = lane % 16, g = lane / 16, wave = threadIdx.x / kWave;
-  const int block = blockIdx.x % row_blocks;
-  const int64_t t0 = (int64_t)(blockIdx.x / row_blocks) * TT;
-  load_tokad<TT, kThreads>(a, t0, tok);
-  stage_u<TT, kThreads>(a, a.du, slices, t0, us);
-  __syncthreads();
-  const UOperand<T, Q, STEPS, SMALL> u(a, us);
-  int ra[Q][4];
-  row_adapters<Q>(tok, ra);
-  const int64_t f_end0 = (int64_t)(block + 1) * rows_per_block;
-  const int64_t f_end = f_end0 < a.n_in ? f_end0 : a.n_in;
-  const int64_t left = a.T - t0;
-  T* out = (T*)a.out + t0;
-  for (int64_t fb = (int64_t)block * rows_per_block + wave * 16 * V; fb < f_end;
-       fb += kWaves * 16 * V) {
-    const int64_t f = fb + n * V < a.n_in - V ? fb + n * V : a.n_in - V;
-    f32x4 res[V][Q];
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-#pragma unroll
-      for (int q = 0; q < Q; ++q) res[j][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-    AdapterWalk<TT> walk(tok);
-    int ad;
-    while (walk.next(ad)) {
-      const int rank = rank_of(a, ad);
-      const T* A = (const T*)a.A + (int64_t)ad * a.R * a.n_in + f;
-      f32x4 acc[V][Q];
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int q = 0; q < Q; ++q) acc[j][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const int blocks = STEPS > 0 ? STEPS : u.blocks;
-      for (int k = 0; k < blocks; ++k) {
-        const int r = rank_base<T, SMALL>(k);
-        Row<T, V> rows[8];
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          zero_row(rows[s]);
-          if (s < KR && r + s < rank) rows[s] = load_row<T, V>(A + (int64_t)(r + s) * a.n_in);
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) u.product(k, column<T, V>(rows, j), acc[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            res[j][q][i] = ra[q][i] == ad ? acc[j][q][i] * u.up[q][i] : res[j][q][i];
-    }
-    if (fb + n * V < a.n_in) {
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const int t = p * 4 * C + g * C;
-          float v[C];
-#pragma unroll
-          for (int e = 0; e < C; ++e) v[e] = res[j][(p * C + e) / 4][e % 4];
-          store_chunk<T, C>(out + (f + j) * a.ldo + t, clampi(left - t, 0, C), v);
-        }
-    }
-  }
+  __shared__ TileAdapters<TT> tile;
+  const int64_t t0 = (int64_t)(blockIdx.x % tiles) * TT;
+  const int64_t row0 = (int64_t)(blockIdx.x / tiles) * rows_per_block;
+  const int64_t end = row0 + rows_per_block < a.n_out ? row0 + rows_per_block : a.n_out;
+  if constexpr (V == 1) stage_u<TT, kThreads>(a, a.u, slices, t0, us);
+  tile_adapters<TT, kThreads>(a, t0, tile);
+  stream_rows<T, V, STEPS, SMALL, V != 1, false>(a, tile, us, t0, row0, end);
 }
 
 // ------------------------------------------------------------------ outer --
 
+constexpr int kOuterFeatures = 2;   // 16-feature rows of tiles a workgroup takes
+constexpr int kListTokens = 32 * kThreads;
+
+template <int FF, int NR>
+struct OuterShared {
+  f32x4 red[kWaves / 2 * FF * NR * kWave];
+  uint32_t mask[kThreads];
+  uint16_t block[kThreads];
+  int waves[kWaves];
+};
+
 // dA_a = sum over the adapter's tokens of du x^T, and dB_a = sum of dy u^T:
 // one workgroup takes 16 FF features of x (or of dy), one adapter and up to 64
-// ranks.  Its waves walk the 32-token blocks in turn, skip those without a
-// token of the adapter, and mask the others' tokens out of both operands; the
-// waves' sums are added in a fixed order.  f16: u's block is scaled by rank
-// (its largest |u| among the block's tokens of this adapter), and the block's
-// product is scaled back in fp32.
-template <typename T, int FF, int NR>
-__global__ __launch_bounds__(kOuterThreads) void lowrank_outer_kernel(LowRankArgs a, int xblocks) {
-  __shared__ f32x4 red[kOuterWaves / 2 * FF * NR * kWave];
-  const int lane = lane_id(), n = lane % 16, g = lane / 16, wave = threadIdx.x / kWave;
-  const bool is_x = (int)blockIdx.x < xblocks;
+// ranks.  It lists the 32-token blocks that hold a token of the adapter, its
+// waves take them in turn, two together where registers allow, the next ones'
+// loads in flight; other adapters' tokens are masked out of both operands.
+// The waves' sums are added in a fixed order.  f16: the block's product is
+// scaled back in fp32 by the exponent that pack chose for the rank.
+template <typename T, int NR>
+__device__ __forceinline__ void outer_tile(const LowRankArgs& a, bool is_x, int64_t f0, int ad,
+                                           int r0, OuterShared<kOuterFeatures, NR>& sh) {
+  constexpr int FF = kOuterFeatures, P = NR * sizeof(T) > 4 ? 1 : 2;
+  constexpr bool F16 = __is_same(T, _Float16), HALVES = sizeof(T) == 2;
+  const int tid = threadIdx.x, lane = lane_id(), n = lane % 16, g = lane / 16, wave = tid / kWave;
   const int64_t F = is_x ? a.n_in : a.n_out, ld = is_x ? a.ldx : a.ldy;
   const T* src = (const T*)(is_x ? a.x : a.y);
-  const float* u = is_x ? a.du : a.u;
-  const int64_t f0 = (int64_t)(is_x ? blockIdx.x : blockIdx.x - xblocks) * (16 * FF);
-  const int ad = blockIdx.y, r0 = blockIdx.z * 64;
+  const T* u = (const T*)(is_x ? a.rdu : a.ru);
+  const uint8_t* ex = is_x ? a.edu : a.eu;
+  const int64_t half = (int64_t)a.R * a.Tp;
   const T* row[FF];
 #pragma unroll
   for (int k = 0; k < FF; ++k) {
     const int64_t f = f0 + k * 16 + n;
     row[k] = src + (f < F ? f : F - 1) * ld;
   }
-  const float* urow[NR];
+  int64_t urow[NR];
 #pragma unroll
   for (int q = 0; q < NR; ++q) {
     const int r = r0 + q * 16 + n;
-    urow[q] = u + (int64_t)(r < a.R ? r : a.R - 1) * a.Tp;
+    urow[q] = (int64_t)(r < a.R ? r : a.R - 1) * a.Tp;
   }
   f32x4 acc[FF * NR];
 #pragma unroll
   for (int k = 0; k < FF * NR; ++k) acc[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int64_t blocks = cdiv(a.T, 32);
-  for (int64_t b = wave; b < blocks; b += kOuterWaves) {
-    const int64_t t = b * 32 + g * 8;
-    const int cnt = clampi(a.T - t, 0, 8);
+  struct Buf {
+    Frag<T> x[P][FF], hi[P][NR], lo[P][HALVES ? NR : 1];
+    uint32_t e[P][F16 ? NR : 1], m[P];
+  } cur, nxt;
+  for (int64_t c0 = 0; c0 < a.T; c0 += kListTokens) {
+    // this chunk's blocks with a token of the adapter
     uint32_t m = 0;
-    if (cnt == 8) {
-      int ta[8];
-      __builtin_memcpy(ta, __builtin_assume_aligned(a.tokad + t, 16), sizeof(ta));
+    const int64_t tb = c0 + (int64_t)tid * 32;
+    if (tb < a.T) {
+      int ta[32];
+      __builtin_memcpy(ta, __builtin_assume_aligned(a.tokad + tb, 16), sizeof(ta));
+      const int left = clampi(a.T - tb, 0, 32);
 #pragma unroll
-      for (int s = 0; s < 8; ++s) m |= (ta[s] == ad ? 1u : 0u) << s;
-    } else {
-      for (int s = 0; s < cnt; ++s) m |= (a.tokad[t + s] == ad ? 1u : 0u) << s;
+      for (int s = 0; s < 32; ++s) m |= (ta[s] == ad && s < left ? 1u : 0u) << s;
     }
-    if (__ballot(m != 0) == 0) continue;
-    Frag<T> fx[FF];
+    const uint64_t any = __ballot(m != 0);
+    if (lane == 0) sh.waves[wave] = __builtin_popcountll(any);
+    sh.mask[tid] = m;
+    __syncthreads();
+    int before = 0, count = 0;
 #pragma unroll
-    for (int k = 0; k < FF; ++k) fx[k] = cnt == 8 ? load8(row[k] + t) : load8_count(row[k] + t, cnt);
-    float uv[NR][8];
-#pragma unroll
-    for (int q = 0; q < NR; ++q)
-      __builtin_memcpy(uv[q], __builtin_assume_aligned(urow[q] + t, 16), sizeof(uv[q]));
-    if (__ballot(m != 255u) != 0) {
-#pragma unroll
-      for (int k = 0; k < FF; ++k) mask8(fx[k], m);
-#pragma unroll
-      for (int q = 0; q < NR; ++q)
-#pragma unroll
-        for (int s = 0; s < 8; ++s) uv[q][s] = (m >> s) & 1u ? uv[q][s] : 0.f;
+    for (int w = 0; w < kWaves; ++w) {
+      before += w < wave ? sh.waves[w] : 0;
+      count += sh.waves[w];
     }
+    if (m != 0) sh.block[before + __builtin_popcountll(any & lanemask_lt())] = (uint16_t)tid;
+    __syncthreads();
+    count = __builtin_amdgcn_readfirstlane(count);
+    auto load = [&](int e, Buf& b) {
 #pragma unroll
-    for (int q = 0; q < NR; ++q) {
-      if constexpr (__is_same(T, _Float16)) {
-        float big = 0.f;
+      for (int p = 0; p < P; ++p) {
+        const int at = e + p < count ? e + p : count - 1;
+        const int blk = __builtin_amdgcn_readfirstlane((int)sh.block[at]);
+        b.m[p] = e + p < count ? __builtin_amdgcn_readfirstlane(sh.mask[blk]) : 0u;
+        const int64_t bt = c0 + (int64_t)blk * 32, t = bt + g * 8;
+        const bool whole = bt + 32 <= a.T;
 #pragma unroll
-        for (int s = 0; s < 8; ++s) big = fmaxf(big, fabsf(uv[q][s]));
-        big = fmaxf(big, __shfl_xor(big, 16, kWave));
-        big = fmaxf(big, __shfl_xor(big, 32, kWave));
-        const Pow2 p = pow2_of(big);
+        for (int k = 0; k < FF; ++k)
+          b.x[p][k] = whole ? load8(row[k] + t) : load8_count(row[k] + t, clampi(a.T - t, 0, 8));
 #pragma unroll
-        for (int s = 0; s < 8; ++s) uv[q][s] *= p.down;
-        const Frag<T> hi = split8<T>(uv[q], false), lo = split8<T>(uv[q], true);
-#pragma unroll
-        for (int k = 0; k < FF; ++k) {
-          const f32x4 c = mma(fx[k], lo, mma(fx[k], hi, f32x4{0.f, 0.f, 0.f, 0.f}));
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[k * NR + q][i] = __builtin_fmaf(c[i], p.up, acc[k * NR + q][i]);
-        }
-      } else {
-        const Frag<T> hi = split8<T>(uv[q], false);
-#pragma unroll
-        for (int k = 0; k < FF; ++k) acc[k * NR + q] = mma(fx[k], hi, acc[k * NR + q]);
-        if constexpr (sizeof(T) == 2) {
-          const Frag<T> lo = split8<T>(uv[q], true);
-#pragma unroll
-          for (int k = 0; k < FF; ++k) acc[k * NR + q] = mma(fx[k], lo, acc[k * NR + q]);
+        for (int q = 0; q < NR; ++q) {
+          __builtin_memcpy(&b.hi[p][q], __builtin_assume_aligned(u + urow[q] + t, 16),
+                           sizeof(Frag<T>));
+          if constexpr (HALVES)
+            __builtin_memcpy(&b.lo[p][q], __builtin_assume_aligned(u + half + urow[q] + t, 16),
+                             sizeof(Frag<T>));
+          // any token of the adapter in the block has the scale
+          if constexpr (F16) b.e[p][q] = ex[urow[q] + bt + (b.m[p] ? __builtin_ctz(b.m[p]) : 0)];
         }
       }
+    };
+    auto compute = [&](Buf& b) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (b.m[p] == 0) continue;
+        if (b.m[p] != ~0u) {
+          const uint32_t m8 = (b.m[p] >> (g * 8)) & 255u;
+#pragma unroll
+          for (int k = 0; k < FF; ++k) mask8(b.x[p][k], m8);
+#pragma unroll
+          for (int q = 0; q < NR; ++q) {
+            mask8(b.hi[p][q], m8);
+            if constexpr (HALVES) mask8(b.lo[p][q], m8);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < NR; ++q)
+#pragma unroll
+          for (int k = 0; k < FF; ++k) {
+            f32x4& d = acc[k * NR + q];
+            if constexpr (F16) {
+              const float up = __uint_as_float(b.e[p][q] << 23);
+              const f32x4 c = mma(b.x[p][k], b.lo[p][q],
+                                  mma(b.x[p][k], b.hi[p][q], f32x4{0.f, 0.f, 0.f, 0.f}));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) d[i] = __builtin_fmaf(c[i], up, d[i]);
+            } else {
+              d = mma(b.x[p][k], b.hi[p][q], d);
+              if constexpr (HALVES) d = mma(b.x[p][k], b.lo[p][q], d);
+            }
+          }
+      }
+    };
+    if (wave * P < count) load(wave * P, nxt);
+    for (int e = wave * P; e < count; e += kWaves * P) {
+      cur = nxt;
+      if (e + kWaves * P < count) load(e + kWaves * P, nxt);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(cur);
     }
+    __syncthreads();
   }
-  wave_tree_sum<FF * NR, kOuterWaves>(acc, red);
+  wave_tree_sum<FF * NR, kWaves>(acc, sh.red);
   if (wave != 0) return;
   const int rank = rank_of(a, ad);
   T* out = (T*)(is_x ? a.dA : a.dB) + (int64_t)ad * a.R * F;
@@ -745,6 +968,32 @@ __global__ __launch_bounds__(kOuterThreads) void lowrank_outer_kernel(LowRankArg
     }
 }
 
+// dA, dB and dx in one launch: they need the same packed ranks and nothing of
+// each other, and the reads of the first two go beside the writes of the last.
+template <typename T, int NR, int STEPS, bool SMALL>
+__global__ __launch_bounds__(kThreads) void lowrank_gradients_kernel(LowRankArgs a, int xblocks,
+                                                                     int yblocks, int tiles,
+                                                                     int rows_per_block) {
+  constexpr int V = 16 / sizeof(T), TT = 16 * V, FF = kOuterFeatures;
+  __shared__ union {
+    OuterShared<FF, NR> outer;
+    TileAdapters<TT> tile;
+  } sh;
+  const int rcs = (a.R + 63) / 64;
+  const int64_t outer = (int64_t)(xblocks + yblocks) * a.n * rcs;
+  if (blockIdx.x < outer) {
+    const int per = a.n * rcs, fb = blockIdx.x / per, rest = blockIdx.x % per;
+    const bool is_x = fb < xblocks;
+    outer_tile<T, NR>(a, is_x, (int64_t)(is_x ? fb : fb - xblocks) * (16 * FF), rest / rcs,
+                      rest % rcs * 64, sh.outer);
+  } else {
+    const int64_t b = blockIdx.x - outer, t0 = b % tiles * TT, row0 = b / tiles * rows_per_block;
+    const int64_t end = row0 + rows_per_block < a.n_in ? row0 + rows_per_block : a.n_in;
+    tile_adapters<TT, kThreads>(a, t0, sh.tile);
+    stream_rows<T, V, STEPS, SMALL, true, true>(a, sh.tile, nullptr, t0, row0, end);
+  }
+}
+
 // ---------------------------------------------------------------- project --
 
 // y = W x + B u on a tile of 16 V tokens: a workgroup takes 16 MO rows of W,
@@ -752,21 +1001,21 @@ __global__ __launch_bounds__(kOuterThreads) void lowrank_outer_kernel(LowRankArg
 // shrink kernel packed.  The waves' sums meet in shared memory, where the
 // adapters' part is added.
 template <typename T, int V, int MO, bool SMALL>
-__global__ __launch_bounds__(kOuterThreads) void lowrank_project_kernel(LowRankArgs a, int slices,
+__global__ __launch_bounds__(kProjectThreads) void lowrank_project_kernel(LowRankArgs a, int slices,
                                                                         int row_blocks) {
   constexpr int TT = 16 * V;
   extern __shared__ float us[];
-  __shared__ f32x4 red[kOuterWaves * MO * V * kWave];
+  __shared__ f32x4 red[kProjectWaves * MO * V * kWave];
   __shared__ int tok[TT];
   const int lane = lane_id(), n = lane % 16, g = lane / 16, wave = threadIdx.x / kWave;
   const int block = blockIdx.x % row_blocks;
   const int64_t tile = blockIdx.x / row_blocks;
   int64_t t0 = tile * TT;
   if (t0 > a.T - TT) t0 = a.T > TT ? a.T - TT : 0;
-  load_tokad<TT, kOuterThreads>(a, t0, tok);
-  stage_u<TT, kOuterThreads>(a, a.u, slices, t0, us);
+  load_tokad<TT, kProjectThreads>(a, t0, tok);
+  stage_u<TT, kProjectThreads>(a, a.u, slices, t0, us);
   const int64_t steps = cdiv(a.n_in, 32);
-  const int64_t s0 = steps * wave / kOuterWaves, s1 = steps * (wave + 1) / kOuterWaves;
+  const int64_t s0 = steps * wave / kProjectWaves, s1 = steps * (wave + 1) / kProjectWaves;
   const int64_t o0 = (int64_t)block * (16 * MO);
   const T* w[MO];
 #pragma unroll
@@ -779,18 +1028,30 @@ __global__ __launch_bounds__(kOuterThreads) void lowrank_project_kernel(LowRankA
 #pragma unroll
   for (int k = 0; k < MO * V; ++k) acc[k] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int64_t whole = a.n_in / 32 < s1 ? a.n_in / 32 : s1;
+  // U steps' loads are issued together: a wave alone keeps U (MO + V) KB (f16)
+  // in flight, and the eight waves of a workgroup cover the latency of HBM
+  constexpr int U = 8 / V;
+  auto run = [&](int64_t at, auto steps_together) {
+    constexpr int N = decltype(steps_together)::value;
+    Frag<T> fw[N][MO], fx[N][V];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+      for (int k = 0; k < MO; ++k) fw[i][k] = load8(w[k] + (at + i) * 32 + g * 8);
+#pragma unroll
+      for (int j = 0; j < V; ++j) fx[i][j] = load8(xp + ((at + i) * V + j) * kWave * 8);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // or the loads are spread among the products
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int k = 0; k < MO; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[k * V + j] = mma(fx[i][j], fw[i][k], acc[k * V + j]);
+  };
   int64_t s = s0;
-  for (; s < whole; ++s) {
-    Frag<T> fw[MO], fx[V];
-#pragma unroll
-    for (int k = 0; k < MO; ++k) fw[k] = load8(w[k] + s * 32 + g * 8);
-#pragma unroll
-    for (int j = 0; j < V; ++j) fx[j] = load8(xp + (s * V + j) * kWave * 8);
-#pragma unroll
-    for (int k = 0; k < MO; ++k)
-#pragma unroll
-      for (int j = 0; j < V; ++j) acc[k * V + j] = mma(fx[j], fw[k], acc[k * V + j]);
-  }
+  for (; s + U <= whole; s += U) run(s, Int<U>{});
+  for (; s < whole; ++s) run(s, Int<1>{});
   if (s < s1) {
     const int cnt = clampi(a.n_in - s * 32 - g * 8, 0, 8);
 #pragma unroll
@@ -806,10 +1067,10 @@ __global__ __launch_bounds__(kOuterThreads) void lowrank_project_kernel(LowRankA
   __syncthreads();
   const int64_t lim = a.T - V;
   const int blocks = SMALL ? 1 : (a.R + 31) / 32;
-  for (int k = wave; k < MO * V; k += kOuterWaves) {
+  for (int k = wave; k < MO * V; k += kProjectWaves) {
     f32x4 v = red[k * kWave + lane];
 #pragma unroll
-    for (int h = 1; h < kOuterWaves; ++h) v += red[(h * MO * V + k) * kWave + lane];
+    for (int h = 1; h < kProjectWaves; ++h) v += red[(h * MO * V + k) * kWave + lane];
     const int j = k % V;
     const int64_t o = o0 + k / V * 16 + n, oc = o < a.n_out ? o : a.n_out - 1;
     auto local = [&](int m) {
@@ -826,7 +1087,7 @@ __global__ __launch_bounds__(kOuterThreads) void lowrank_project_kernel(LowRankA
       for (int b = 0; b < blocks; ++b) {
         const Frag<T> hi = u_frag<T, SMALL>(row, b, false, p.down);
         const Frag<T> lo = u_frag<T, SMALL>(row, b, true, p.down);
-        c = u_mma<T, SMALL>(hi, lo, b_frag<T, SMALL>(a, ad, oc, rank, b), c);
+        c = token_mma<T, SMALL>(hi, lo, b_frag<T, SMALL>(a, ad, oc, rank, b), c);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -903,66 +1164,68 @@ hipError_t shrink(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
 
 size_t staged_bytes(int64_t tokens, int R) { return (size_t)tokens * staged_width(R) * 4; }
 
-// Rows a workgroup of expand or dx takes: enough that staging u is a small
-// part of the streams, few enough that the launch fills the GPU.
-int64_t rows_per_block(int64_t rows, int64_t tiles, int64_t unit) {
-  int64_t blocks = cdiv(4 * kFillBlocks, tiles);
-  int64_t per = cdiv(cdiv(rows, blocks), unit) * unit;
-  return per < 512 ? per : cdiv(512, unit) * unit;
+// Rows a workgroup of expand or dx takes: enough that loading its tokens'
+// ranks is a small part of the streams, few enough that the launch fills the
+// GPU.
+int64_t rows_per_block(int64_t rows, int64_t tiles) {
+  const int64_t unit = 16 * kWaves, blocks = cdiv(4 * kFillBlocks, tiles);
+  const int64_t per = cdiv(cdiv(rows, blocks), unit) * unit;
+  return per < 512 ? per : 512;
 }
 
-template <typename T, int Q>
-hipError_t expand_q(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
-  const int64_t tiles = cdiv(a.T, 16 * Q), per = rows_per_block(a.n_out, tiles, 16 * kWaves);
-  const int64_t rb = cdiv(a.n_out, per);
-  const dim3 grid((unsigned)(rb * tiles));
-  const size_t lds = staged_bytes(16 * Q, a.R);
-  if (a.R <= 16)
-    hipLaunchKernelGGL((lowrank_expand_kernel<T, Q, 1, true>), grid, dim3(kThreads), lds, s, a,
-                       l.slices_u, (int)per, (int)rb);
-  else if (a.R <= 32)
-    hipLaunchKernelGGL((lowrank_expand_kernel<T, Q, 1, false>), grid, dim3(kThreads), lds, s, a,
-                       l.slices_u, (int)per, (int)rb);
-  else if (a.R <= 64)
-    hipLaunchKernelGGL((lowrank_expand_kernel<T, Q, 2, false>), grid, dim3(kThreads), lds, s, a,
-                       l.slices_u, (int)per, (int)rb);
-  else
-    hipLaunchKernelGGL((lowrank_expand_kernel<T, Q, 0, false>), grid, dim3(kThreads), lds, s, a,
-                       l.slices_u, (int)per, (int)rb);
+// Tokens up to this many go through expand 16 to a tile, without the pack
+// launch.
+constexpr int64_t kStagedTokens = 128;
+
+bool packs(int op, int64_t T) { return op == kLowRankBackward || (op == kLowRankAdd && T > kStagedTokens); }
+
+template <typename T, bool BACKWARD>
+hipError_t pack(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
+  const dim3 grid((unsigned)(a.Tp / kPackTokens), BACKWARD ? 2 : 1);
+  hipLaunchKernelGGL((lowrank_pack_kernel<T, BACKWARD>), grid, dim3(kThreads),
+                     (size_t)a.R * (kPackTokens + 1) * 4, s, a, l.slices_u, l.slices_du);
   return hipGetLastError();
 }
 
-template <typename T, int Q, int V>
-hipError_t dx_qv(const LowRankArgs& a, hipStream_t s) {
-  const int64_t tiles = cdiv(a.T, 16 * Q), per = rows_per_block(a.n_in, tiles, 16 * V * kWaves);
-  const int64_t rb = cdiv(a.n_in, per);
-  const dim3 grid((unsigned)(rb * tiles));
-  const size_t lds = staged_bytes(16 * Q, a.R);
+template <typename T, int V>
+hipError_t expand_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
+  const int64_t tiles = cdiv(a.T, 16 * V), per = rows_per_block(a.n_out, tiles);
+  const dim3 grid((unsigned)(cdiv(a.n_out, per) * tiles));
+  const size_t lds = V == 1 ? staged_bytes(16, a.R) : 0;
   if (a.R <= 16)
-    hipLaunchKernelGGL((lowrank_dx_kernel<T, Q, V, 1, true>), grid, dim3(kThreads), lds, s, a, 1,
-                       (int)per, (int)rb);
+    hipLaunchKernelGGL((lowrank_expand_kernel<T, V, 1, true>), grid, dim3(kThreads), lds, s, a,
+                       l.slices_u, (int)tiles, (int)per);
   else if (a.R <= 32)
-    hipLaunchKernelGGL((lowrank_dx_kernel<T, Q, V, 1, false>), grid, dim3(kThreads), lds, s, a, 1,
-                       (int)per, (int)rb);
+    hipLaunchKernelGGL((lowrank_expand_kernel<T, V, 1, false>), grid, dim3(kThreads), lds, s, a,
+                       l.slices_u, (int)tiles, (int)per);
   else if (a.R <= 64)
-    hipLaunchKernelGGL((lowrank_dx_kernel<T, Q, V, 2, false>), grid, dim3(kThreads), lds, s, a, 1,
-                       (int)per, (int)rb);
+    hipLaunchKernelGGL((lowrank_expand_kernel<T, V, 2, false>), grid, dim3(kThreads), lds, s, a,
+                       l.slices_u, (int)tiles, (int)per);
   else
-    hipLaunchKernelGGL((lowrank_dx_kernel<T, Q, V, 0, false>), grid, dim3(kThreads), lds, s, a, 1,
-                       (int)per, (int)rb);
+    hipLaunchKernelGGL((lowrank_expand_kernel<T, V, 0, false>), grid, dim3(kThreads), lds, s, a,
+                       l.slices_u, (int)tiles, (int)per);
   return hipGetLastError();
 }
 
-template <typename T, int FF>
-hipError_t outer_f(const LowRankArgs& a, hipStream_t s) {
-  const int xblocks = (int)cdiv(a.n_in, 16 * FF), yblocks = (int)cdiv(a.n_out, 16 * FF);
-  const dim3 grid((unsigned)(xblocks + yblocks), (unsigned)a.n, (unsigned)cdiv(a.R, 64));
+template <typename T>
+hipError_t gradients(const LowRankArgs& a, hipStream_t s) {
+  constexpr int TT = 256 / sizeof(T);
+  const int64_t xb = cdiv(a.n_in, 16 * kOuterFeatures), yb = cdiv(a.n_out, 16 * kOuterFeatures);
+  const int64_t tiles = cdiv(a.T, TT), per = rows_per_block(a.n_in, tiles > 0 ? tiles : 1);
+  const dim3 grid((unsigned)((xb + yb) * a.n * cdiv(a.R, 64) + cdiv(a.n_in, per) * tiles));
+  const int t = (int)(tiles > 0 ? tiles : 1);
   if (a.R <= 16)
-    hipLaunchKernelGGL((lowrank_outer_kernel<T, FF, 1>), grid, dim3(kOuterThreads), 0, s, a, xblocks);
+    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 1, 1, true>), grid, dim3(kThreads), 0, s, a,
+                       (int)xb, (int)yb, t, (int)per);
   else if (a.R <= 32)
-    hipLaunchKernelGGL((lowrank_outer_kernel<T, FF, 2>), grid, dim3(kOuterThreads), 0, s, a, xblocks);
+    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 2, 1, false>), grid, dim3(kThreads), 0, s, a,
+                       (int)xb, (int)yb, t, (int)per);
+  else if (a.R <= 64)
+    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 4, 2, false>), grid, dim3(kThreads), 0, s, a,
+                       (int)xb, (int)yb, t, (int)per);
   else
-    hipLaunchKernelGGL((lowrank_outer_kernel<T, FF, 4>), grid, dim3(kOuterThreads), 0, s, a, xblocks);
+    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 4, 0, false>), grid, dim3(kThreads), 0, s, a,
+                       (int)xb, (int)yb, t, (int)per);
   return hipGetLastError();
 }
 
@@ -972,10 +1235,10 @@ hipError_t project_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s
   const dim3 grid((unsigned)(rb * cdiv(a.T, 16 * V)));
   const size_t lds = staged_bytes(16 * V, a.R);
   if (a.R <= 16)
-    hipLaunchKernelGGL((lowrank_project_kernel<T, V, MO, true>), grid, dim3(kOuterThreads), lds, s,
+    hipLaunchKernelGGL((lowrank_project_kernel<T, V, MO, true>), grid, dim3(kProjectThreads), lds, s,
                        a, l.slices_u, (int)rb);
   else
-    hipLaunchKernelGGL((lowrank_project_kernel<T, V, MO, false>), grid, dim3(kOuterThreads), lds, s,
+    hipLaunchKernelGGL((lowrank_project_kernel<T, V, MO, false>), grid, dim3(kProjectThreads), lds, s,
                        a, l.slices_u, (int)rb);
   return hipGetLastError();
 }
@@ -984,22 +1247,19 @@ template <typename T>
 hipError_t add_t(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
   hipError_t e = shrink<T, false, false>(a, l, s);
   if (e != hipSuccess) return e;
-  return a.T <= 16 * 8 ? expand_q<T, 1>(a, l, s) : expand_q<T, 4>(a, l, s);
+  if (!packs(kLowRankAdd, a.T)) return expand_v<T, 1>(a, l, s);
+  if ((e = pack<T, false>(a, l, s)) != hipSuccess) return e;
+  return expand_v<T, 16 / sizeof(T)>(a, l, s);
 }
 
 template <typename T>
 hipError_t backward_t(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
-  if (a.T == 0) return outer_f<T, 2>(a, s);  // zeros
-  hipError_t e = shrink<T, true, false>(a, l, s);
-  if (e != hipSuccess) return e;
-  if (l.slices_u > 1 || l.slices_du > 1) {
-    const dim3 grid((unsigned)cdiv((int64_t)a.R * a.Tp, 4 * kThreads), 2);
-    hipLaunchKernelGGL(lowrank_join_kernel, grid, dim3(kThreads), 0, s, a, l.slices_u, l.slices_du);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (a.T > 0) {
+    hipError_t e = shrink<T, true, false>(a, l, s);
+    if (e != hipSuccess) return e;
+    if ((e = pack<T, true>(a, l, s)) != hipSuccess) return e;
   }
-  e = a.n_in < 4 ? dx_qv<T, 4, 1>(a, s) : dx_qv<T, 4, 4>(a, s);
-  if (e != hipSuccess) return e;
-  return outer_f<T, 2>(a, s);
+  return gradients<T>(a, s);  // zeros where there are no tokens
 }
 
 template <typename T>
@@ -1019,7 +1279,7 @@ LowRankLayout lowrank_layout(int op, int dtype, int64_t T, int64_t S, int64_t n,
                              int64_t n_in, int64_t n_out) {
   LowRankLayout l{};
   const int64_t eb = dtype == kF32 ? 4 : 2;
-  l.Tp = cdiv(T, 32) * 32;
+  l.Tp = cdiv(T, 128) * 128;  // whole tiles
   l.width = token_width(op, dtype, T);
   l.groups = adapter_groups(T, S, n, 16 * l.width);
   const int64_t tiles = cdiv(T, 16 * l.width);
@@ -1038,6 +1298,13 @@ LowRankLayout lowrank_layout(int op, int dtype, int64_t T, int64_t S, int64_t n,
   l.at_packed = take(op == kLowRankProject
                          ? (size_t)(tiles * cdiv(n_in, 32) * l.width * kWave * 8 * eb)
                          : 0);
+  const bool rows = packs(op, T), sides = op == kLowRankBackward;
+  l.at_rows = take(rows ? (size_t)l.Tp * packed_row((int)R) : 0);
+  l.at_up = take(rows ? (size_t)l.Tp * 4 : 0);
+  l.at_ru = take(sides ? (size_t)R * l.Tp * 4 : 0);
+  l.at_rdu = take(sides ? (size_t)R * l.Tp * 4 : 0);
+  l.at_eu = take(sides ? (size_t)R * l.Tp : 0);
+  l.at_edu = take(sides ? (size_t)R * l.Tp : 0);
   l.bytes = at;
   return l;
 }
@@ -1050,6 +1317,12 @@ hipError_t launch_lowrank(int op, int dtype, LowRankArgs a, void* ws, hipStream_
   a.u = (float*)(w + l.at_u);
   a.du = (float*)(w + l.at_du);
   a.packed = w + l.at_packed;
+  a.rows = w + l.at_rows;
+  a.up = (float*)(w + l.at_up);
+  a.ru = w + l.at_ru;
+  a.rdu = w + l.at_rdu;
+  a.eu = (uint8_t*)(w + l.at_eu);
+  a.edu = (uint8_t*)(w + l.at_edu);
   switch (dtype) {
     case kF32:
       return op == kLowRankAdd ? add_t<float>(a, l, s)
