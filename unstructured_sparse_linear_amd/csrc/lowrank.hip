@@ -44,6 +44,13 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kProjectThreads = 512;  // project: eight waves
 constexpr int kProjectWaves = kProjectThreads / kWave;
 
+// Workgroup b of N runs on XCD b % 8.  Each XCD takes one contiguous part of
+// the work list: neighbouring tiles share lines, factors and pages of one L2.
+__device__ __forceinline__ uint32_t xcd_chunk(uint32_t b, uint32_t N) {
+  const uint32_t x = b % 8, q = N / 8, r = N % 8;
+  return x * q + (x < r ? x : r) + b / 8;
+}
+
 // ------------------------------------------------------ adapters of tokens --
 
 template <int TT>
@@ -229,17 +236,18 @@ __device__ __forceinline__ void shrink_steps(const T* x, int64_t ldx, int64_t K,
 
 template <typename T, int V, int NR, bool TR, bool PACK>
 __device__ __forceinline__ void shrink_tile(const LowRankArgs& a, const ShrinkJob& job, int slice,
-                                            int groups, f32x4* red, TokenTile<16 * V>& tile) {
+                                            int tile_id, int part, bool first, int groups,
+                                            f32x4* red, TokenTile<16 * V>& tile) {
   constexpr int TT = 16 * V;
   const int lane = lane_id(), n = lane % 16, g = lane / 16, wave = threadIdx.x / kWave;
   // the last tile is moved back to end at T (its shared tokens get the same
   // values twice), and a lane's V tokens are moved back likewise: no load
   // passes the end of a row
-  int64_t t0 = (int64_t)blockIdx.x * TT;
+  int64_t t0 = (int64_t)tile_id * TT;
   if (t0 > a.T - TT) t0 = a.T > TT ? a.T - TT : 0;
   token_adapters<TT, kThreads>(a, t0, tile);
-  const int rc = blockIdx.y / groups, group = blockIdx.y % groups;
-  if (blockIdx.y == 0 && blockIdx.z == 0)
+  const int rc = part / groups, group = part % groups;
+  if (first)
     for (int t = threadIdx.x; t < TT; t += kThreads)
       if (t0 + t < a.T) a.tokad[t0 + t] = tile.tok[t];
   const int64_t lim = a.T - V;
@@ -249,8 +257,8 @@ __device__ __forceinline__ void shrink_tile(const LowRankArgs& a, const ShrinkJo
   const int64_t s0 = steps * unit / units, s1 = steps * (unit + 1) / units;
   const T* x = (const T*)job.x;
   const int r0 = rc * 64;
-  T* packed = PACK && blockIdx.y == 0
-                  ? (T*)a.packed + (int64_t)blockIdx.x * steps * V * kWave * 8
+  T* packed = PACK && part == 0
+                  ? (T*)a.packed + (int64_t)tile_id * steps * V * kWave * 8
                   : nullptr;
   AdapterWalk<TT> walk(tile.tok);
   int ad, count = 0;
@@ -312,10 +320,16 @@ __global__ __launch_bounds__(kThreads) void lowrank_shrink_kernel(LowRankArgs a,
                                                                   ShrinkJob jy, int groups) {
   __shared__ f32x4 red[kWaves / 2 * NR * V * kWave];
   __shared__ TokenTile<16 * V> tile;
-  if (!BACKWARD || (int)blockIdx.z < jx.slices)
-    shrink_tile<T, V, NR, false, PACK>(a, jx, blockIdx.z, groups, red, tile);
+  // tiles are the fastest index, then the parts of a tile, then the slices
+  const int tiles = (int)((a.T + 16 * V - 1) / (16 * V)), parts = groups * ((a.R + 63) / 64);
+  const uint32_t b = xcd_chunk(blockIdx.x, gridDim.x);
+  const int tile_id = b % tiles, part = b / tiles % parts, z = b / tiles / parts;
+  if (!BACKWARD || z < jx.slices)
+    shrink_tile<T, V, NR, false, PACK>(a, jx, z, tile_id, part, b < (uint32_t)tiles, groups, red,
+                                       tile);
   else
-    shrink_tile<T, V, NR, true, false>(a, jy, blockIdx.z - jx.slices, groups, red, tile);
+    shrink_tile<T, V, NR, true, false>(a, jy, z - jx.slices, tile_id, part, false, groups, red,
+                                       tile);
 }
 
 // ------------------------------------------------------------------- pack --
@@ -797,8 +811,8 @@ __global__ __launch_bounds__(kThreads) void lowrank_expand_kernel(LowRankArgs a,
   constexpr int TT = 16 * V;
   extern __shared__ float us[];
   __shared__ TileAdapters<TT> tile;
-  const int64_t t0 = (int64_t)(blockIdx.x % tiles) * TT;
-  const int64_t row0 = (int64_t)(blockIdx.x / tiles) * rows_per_block;
+  const uint32_t b = xcd_chunk(blockIdx.x, gridDim.x);
+  const int64_t t0 = (int64_t)(b % tiles) * TT, row0 = (int64_t)(b / tiles) * rows_per_block;
   const int64_t end = row0 + rows_per_block < a.n_out ? row0 + rows_per_block : a.n_out;
   if constexpr (V == 1) stage_u<TT, kThreads>(a, a.u, slices, t0, us);
   tile_adapters<TT, kThreads>(a, t0, tile);
@@ -987,7 +1001,7 @@ __global__ __launch_bounds__(kThreads) void lowrank_gradients_kernel(LowRankArgs
     outer_tile<T, NR>(a, is_x, (int64_t)(is_x ? fb : fb - xblocks) * (16 * FF), rest / rcs,
                       rest % rcs * 64, sh.outer);
   } else {
-    const int64_t b = blockIdx.x - outer, t0 = b % tiles * TT, row0 = b / tiles * rows_per_block;
+    const int64_t b = xcd_chunk(blockIdx.x - outer, gridDim.x - outer), t0 = b % tiles * TT, row0 = b / tiles * rows_per_block;
     const int64_t end = row0 + rows_per_block < a.n_in ? row0 + rows_per_block : a.n_in;
     tile_adapters<TT, kThreads>(a, t0, sh.tile);
     stream_rows<T, V, STEPS, SMALL, true, true>(a, sh.tile, nullptr, t0, row0, end);
@@ -1136,8 +1150,8 @@ hipError_t shrink_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s)
   const int rcs = (int)cdiv(a.R, 64);
   ShrinkJob jx{a.x, a.A, a.u, a.ldx, a.n_in, l.slices_u};
   ShrinkJob jy{a.y, a.B, a.du, a.ldy, a.n_out, l.slices_du};
-  const dim3 grid((unsigned)cdiv(a.T, 16 * V), (unsigned)(l.groups * rcs),
-                  (unsigned)(l.slices_u + (BACKWARD ? l.slices_du : 0)));
+  const dim3 grid((unsigned)(cdiv(a.T, 16 * V) * l.groups * rcs *
+                             (l.slices_u + (BACKWARD ? l.slices_du : 0))));
   const int nr = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4;
   if (nr == 1)
     hipLaunchKernelGGL((lowrank_shrink_kernel<T, V, 1, BACKWARD, PACK>), grid, dim3(kThreads), 0, s,
