@@ -74,9 +74,9 @@ __device__ __forceinline__ void token_adapters(const LowRankArgs& a, int64_t t0,
   const int64_t last = t0 + TT < a.T ? t0 + TT : a.T;
   for (int i = tid; i < a.S; i += THREADS) {
     const int64_t b = a.offsets[i], e = a.offsets[i + 1];
+    int ad = a.adapter[i];
     const int64_t lo = b > t0 ? b : t0, hi = e < last ? e : last;
     if (lo < hi) {
-      int ad = a.adapter[i];
       if (ad < 0 || ad >= a.n || (a.ranks && a.ranks[ad] <= 0)) ad = -1;
       const int p = (int)(lo - t0);
       s.mark[p] = p;
@@ -163,74 +163,140 @@ struct ShrinkJob {
   int slices;
 };
 
-// Accumulates 32-feature steps [s0, s1) for the tokens tok..tok+V-1 of each
-// lane and 16 NR ranks from r0.  x is read V tokens wide, eight rows a lane,
-// and turned in registers; the same turn serves a factor stored [K][R].
+// Eight rows of V tokens from p on.
+template <typename T, int V>
+__device__ __forceinline__ void shrink_load(const T* p, int64_t ld, Row<T, V> (&r)[8]) {
+#pragma unroll
+  for (int s = 0; s < 8; ++s) r[s] = load_row<T, V>(p + s * ld);
+}
+// The `left` (0 or less: none) of them that there are, zeros for the rest; the
+// others' addresses are moved back to the last there is.
+template <typename T, int V>
+__device__ __forceinline__ void shrink_load_count(const T* p, int64_t ld, int64_t left,
+                                                  Row<T, V> (&r)[8]) {
+#pragma unroll
+  for (int s = 0; s < 8; ++s) {
+    r[s] = load_row<T, V>(p + (s < left ? s : left - 1) * ld);
+    if (s >= left) zero_row(r[s]);
+    __builtin_amdgcn_sched_barrier(0);  // rare: one address at a time
+  }
+}
+
+// Accumulates the steps [s0, s1) of 32 features for the tokens tok..tok+V-1 of
+// each lane and 16 NR ranks from r0.  x is read V tokens wide, eight rows a
+// lane, and turned in registers; the same turn serves a factor stored [K][R].
+// Two steps' rows are in flight where the sums leave room for them (one alone,
+// at three waves a SIMD: 24 us where two take 19, 67 MB of x and dy, 16 ranks).
 template <typename T, int V, int NR, bool TR, bool PACK>
 __device__ __forceinline__ void shrink_steps(const T* x, int64_t ldx, int64_t K, const T* f, int R,
                                              int r0, int64_t tok, int64_t s0, int64_t s1,
                                              f32x4 (&acc)[NR * V], T* packed) {
   const int lane = lane_id(), n = lane % 16, g = lane / 16;
-  struct Buf {
-    Row<T, V> x[8];
-    Frag<T> f[TR ? 1 : NR];
-    Row<T, TR ? NR : 1> ft[8];
-  } cur, nxt;
-  int64_t frow[NR];
-#pragma unroll
-  for (int b = 0; b < NR; ++b) {
-    const int r = r0 + b * 16 + n;
-    frow[b] = (int64_t)(r < R ? r : R - 1) * K;
-  }
-  const int fcol = TR ? (r0 + n * NR < R - NR ? r0 + n * NR : R - NR) : 0;
-  auto load = [&](int64_t step, Buf& b) {
-    const int64_t k0 = step * 32 + g * 8;
-    const bool whole = step * 32 + 32 <= K;
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const int64_t k = whole || k0 + s < K ? k0 + s : K - 1;
-      b.x[s] = load_row<T, V>(x + k * ldx + tok);
-      if constexpr (TR) b.ft[s] = load_row<T, NR>(f + k * R + fcol);
-    }
-    if constexpr (!TR) {
-#pragma unroll
-      for (int q = 0; q < NR; ++q)
-        b.f[q] = whole ? load8(f + frow[q] + k0)
-                       : load8_count(f + frow[q] + k0, clampi(K - k0, 0, 8));
-    }
-    if (!whole) {
-#pragma unroll
-      for (int s = 0; s < 8; ++s)
-        if (k0 + s >= K) {
-          zero_row(b.x[s]);
-          if constexpr (TR) zero_row(b.ft[s]);
-        }
-    }
-  };
-  auto compute = [&](int64_t step, const Buf& b) {
-    Frag<T> ff[NR];
+  const int64_t k0 = s0 * 32 + g * 8, whole = K / 32 < s1 ? K / 32 : s1;
+  const T* xp = x + k0 * ldx + tok;
+  const T* fp[TR ? 1 : NR];
+  if constexpr (TR) {
+    fp[0] = f + k0 * R + (r0 + n * NR < R - NR ? r0 + n * NR : R - NR);
+  } else {
 #pragma unroll
     for (int q = 0; q < NR; ++q) {
-      if constexpr (TR)
-        ff[q] = column<T, NR>(b.ft, q);
-      else
-        ff[q] = b.f[q];
+      const int r = r0 + q * 16 + n;
+      fp[q] = f + (int64_t)(r < R ? r : R - 1) * K + k0;
     }
+  }
+  constexpr int D = V * NR <= 8 ? 2 : 1;  // steps in flight
+  Row<T, V> xr[D][8];
+  auto compute = [&](int64_t step, const Row<T, V>(&rows)[8], const Frag<T>(&ff)[NR]) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const Frag<T> fx = column<T, V>(b.x, j);
-      if constexpr (PACK) __builtin_memcpy(packed + ((step * V + j) * kWave + lane) * 8, &fx, sizeof(fx));
+      const Frag<T> fx = column<T, V>(rows, j);
+      if (PACK && packed)
+        __builtin_memcpy(packed + ((step * V + j) * kWave + lane) * 8, &fx, sizeof(fx));
 #pragma unroll
       for (int q = 0; q < NR; ++q) acc[q * V + j] = mma(fx, ff[q], acc[q * V + j]);
     }
   };
-  if (s0 >= s1) return;
-  load(s0, cur);
-  for (int64_t s = s0; s < s1; s += 2) {
-    if (s + 1 < s1) load(s + 1, nxt);
-    compute(s, cur);
-    if (s + 2 < s1) load(s + 2, cur);
-    if (s + 1 < s1) compute(s + 1, nxt);
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    if (s0 + d < whole) shrink_load<T, V>(xp, ldx, xr[d]);
+    if (s0 + d < whole) xp += 32 * ldx;
+  }
+#pragma unroll 1
+  for (int64_t at = s0; at < whole; at += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int64_t step = at + d;
+      if (d > 0 && step >= whole) break;
+      Frag<T> ff[NR];
+      if constexpr (TR) {
+        Row<T, NR> ft[8];
+        shrink_load<T, NR>(fp[0], R, ft);
+        fp[0] += 32 * (int64_t)R;
+#pragma unroll
+        for (int q = 0; q < NR; ++q) ff[q] = column<T, NR>(ft, q);
+      } else {
+#pragma unroll
+        for (int q = 0; q < NR; ++q) {
+          ff[q] = load8(fp[q]);
+          fp[q] += 32;
+        }
+      }
+      compute(step, xr[d], ff);
+      if (step + D < whole) {
+        shrink_load<T, V>(xp, ldx, xr[d]);
+        xp += 32 * ldx;
+      }
+    }
+  }
+  if (s0 < s1 && whole < s1) {  // the features past the last 32
+    const int64_t left = K - whole * 32 - g * 8;
+    shrink_load_count<T, V>(xp, ldx, left, xr[0]);
+    Frag<T> ff[NR];
+    if constexpr (TR) {
+      Row<T, NR> ft[8];
+      shrink_load_count<T, NR>(fp[0], R, left, ft);
+#pragma unroll
+      for (int q = 0; q < NR; ++q) ff[q] = column<T, NR>(ft, q);
+    } else {
+#pragma unroll
+      for (int q = 0; q < NR; ++q) ff[q] = load8_count(fp[q], clampi(left, 0, 8));
+    }
+    compute(whole, xr[0], ff);
+  }
+}
+
+// One exchange between the waves w and w ^ BIT: of 2 H tiles each, one ends with
+// the sums of the lower half, the other with those of the upper.
+template <int H, int BIT, int N>
+__device__ __forceinline__ void exchange(f32x4 (&acc)[N], f32x4* red) {
+  const int wave = threadIdx.x / kWave, lane = lane_id();
+  const bool upper = __builtin_amdgcn_readfirstlane(wave & BIT);
+  if (upper) {
+#pragma unroll
+    for (int k = 0; k < H; ++k) {
+      red[(wave * H + k) * kWave + lane] = acc[k];
+      acc[k] = acc[k + H];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < H; ++k) red[(wave * H + k) * kWave + lane] = acc[k + H];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < H; ++k) acc[k] += red[((wave ^ BIT) * H + k) * kWave + lane];
+  __syncthreads();
+}
+
+// Sums the four waves' N tiles: each wave ends with N / 4 of them, in
+// acc[0..N/4), which are tiles wave * N / 4 and on (N >= 4); or wave 0 with all.
+template <int N>
+__device__ __forceinline__ void spread_sum(f32x4 (&acc)[N], f32x4* red) {
+  static_assert(kWaves == 4, "two exchanges");
+  if constexpr (N < 4) {
+    wave_tree_sum<N, kWaves>(acc, red);
+  } else {
+    exchange<N / 2, 2>(acc, red);
+    exchange<N / 4, 1>(acc, red);
   }
 }
 
@@ -238,77 +304,76 @@ template <typename T, int V, int NR, bool TR, bool PACK>
 __device__ __forceinline__ void shrink_tile(const LowRankArgs& a, const ShrinkJob& job, int slice,
                                             int tile_id, int part, bool first, int groups,
                                             f32x4* red, TokenTile<16 * V>& tile) {
-  constexpr int TT = 16 * V;
+  constexpr int TT = 16 * V, N = NR * V;
   const int lane = lane_id(), n = lane % 16, g = lane / 16, wave = threadIdx.x / kWave;
   // the last tile is moved back to end at T (its shared tokens get the same
   // values twice), and a lane's V tokens are moved back likewise: no load
   // passes the end of a row
   int64_t t0 = (int64_t)tile_id * TT;
   if (t0 > a.T - TT) t0 = a.T > TT ? a.T - TT : 0;
-  token_adapters<TT, kThreads>(a, t0, tile);
-  const int rc = part / groups, group = part % groups;
-  if (first)
-    for (int t = threadIdx.x; t < TT; t += kThreads)
-      if (t0 + t < a.T) a.tokad[t0 + t] = tile.tok[t];
   const int64_t lim = a.T - V;
   const int64_t tok = t0 + n * V < lim ? t0 + n * V : lim;
   const int64_t steps = cdiv(job.K, 32), units = (int64_t)job.slices * kWaves;
   const int64_t unit = (int64_t)slice * kWaves + wave;
   const int64_t s0 = steps * unit / units, s1 = steps * (unit + 1) / units;
   const T* x = (const T*)job.x;
+  token_adapters<TT, kThreads>(a, t0, tile);
+  const int rc = part / groups, group = part % groups;
+  if (first)
+    for (int t = threadIdx.x; t < TT; t += kThreads)
+      if (t0 + t < a.T) a.tokad[t0 + t] = tile.tok[t];
   const int r0 = rc * 64;
   T* packed = PACK && part == 0
                   ? (T*)a.packed + (int64_t)tile_id * steps * V * kWave * 8
                   : nullptr;
   AdapterWalk<TT> walk(tile.tok);
-  int ad, count = 0;
-  bool packing = packed != nullptr;
-  // a tile without adapters still packs its x
-  if (packing && walk.done()) {
-    f32x4 acc[NR * V];
+  int count = 0;
+  f32x4 acc[N];
+  for (;;) {
+    int ad = -1;
+    const bool any = walk.next(ad), only = count == 0 && walk.done();
+    if (any && count++ % groups != group) continue;
+    if (!any && !packed) break;  // a tile without adapters still packs its x
 #pragma unroll
-    for (int k = 0; k < NR * V; ++k) acc[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-    shrink_steps<T, V, NR, TR, PACK>(x, job.ldx, job.K, (const T*)job.f, a.R, r0, tok, s0, s1, acc,
-                                     packed);
-  }
-  while (walk.next(ad)) {
-    const bool only = count == 0 && walk.done();
-    if (count++ % groups != group) continue;
-    f32x4 acc[NR * V];
+    for (int k = 0; k < N; ++k) acc[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int64_t from = tok;
+    if (any && !only && !packed) {
+      // lanes without a token of this adapter read along with one that has
+      bool mine = false;
 #pragma unroll
-    for (int k = 0; k < NR * V; ++k) acc[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const T* f = (const T*)job.f + (int64_t)ad * a.R * job.K;
-    if (packing)
-      shrink_steps<T, V, NR, TR, PACK>(x, job.ldx, job.K, f, a.R, r0, tok, s0, s1, acc, packed);
-    else
-      shrink_steps<T, V, NR, TR, false>(x, job.ldx, job.K, f, a.R, r0, tok, s0, s1, acc, nullptr);
-    packing = false;
-    wave_tree_sum<NR * V, kWaves>(acc, red);
-    if (wave == 0) {
-      const float sc = a.scale ? a.scale[ad] : 1.f;
-      const int rank = rank_of(a, ad);
+      for (int j = 0; j < V; ++j) mine |= tile.tok[tok - t0 + j] == ad;
+      const int lead = (int)__builtin_ctzll(__ballot(mine)) % 16;
+      const int64_t there = t0 + lead * V < lim ? t0 + lead * V : lim;
+      from = mine ? tok : there;
+    }
+    shrink_steps<T, V, NR, TR, PACK>(x, job.ldx, job.K,
+                                     (const T*)job.f + (int64_t)(any ? ad : 0) * a.R * job.K, a.R,
+                                     r0, from, s0, s1, acc, packed);
+    packed = nullptr;
+    if (!any) break;
+    spread_sum<N>(acc, red);
+    constexpr int M = N < 4 ? N : N / 4, J = M < V ? M : V;  // tiles of a wave, tokens in a run
+    if (N < 4 && wave != 0) continue;
+    const float sc = a.scale ? a.scale[ad] : 1.f;
+    const int rank = rank_of(a, ad), k0 = N < 4 ? 0 : wave * M;
 #pragma unroll
-      for (int q = 0; q < NR; ++q) {
-        int r;
-        if (TR)
-          r = (r0 + n * NR < a.R - NR ? r0 + n * NR : a.R - NR) + q;
-        else
-          r = r0 + q * 16 + n;
-        if (r >= a.R) continue;
-        float* u = job.u + ((int64_t)slice * a.R + r) * a.Tp;
+    for (int k = 0; k < M; k += J) {
+      const int q = (k0 + k) / V, j0 = (k0 + k) % V;
+      const int r = TR ? (r0 + n * NR < a.R - NR ? r0 + n * NR : a.R - NR) + q : r0 + q * 16 + n;
+      if (r >= a.R) continue;
+      float* u = job.u + ((int64_t)slice * a.R + r) * a.Tp;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t t1 = t0 + (g * 4 + i) * V < lim ? t0 + (g * 4 + i) * V : lim;
-          float v[V];
+      for (int i = 0; i < 4; ++i) {
+        const int64_t t1 = (t0 + (g * 4 + i) * V < lim ? t0 + (g * 4 + i) * V : lim) + j0;
+        float v[J];
 #pragma unroll
-          for (int j = 0; j < V; ++j) v[j] = r < rank ? acc[q * V + j][i] * sc : 0.f;
-          if (only) {
-            __builtin_memcpy(u + t1, v, sizeof(v));
-          } else {
+        for (int j = 0; j < J; ++j) v[j] = r < rank ? acc[k + j][i] * sc : 0.f;
+        if (only) {
+          __builtin_memcpy(u + t1, v, sizeof(v));
+        } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-              if (tile.tok[t1 - t0 + j] == ad) u[t1 + j] = v[j];
-          }
+          for (int j = 0; j < J; ++j)
+            if (tile.tok[t1 - t0 + j] == ad) u[t1 + j] = v[j];
         }
       }
     }
@@ -316,7 +381,7 @@ __device__ __forceinline__ void shrink_tile(const LowRankArgs& a, const ShrinkJo
 }
 
 template <typename T, int V, int NR, bool BACKWARD, bool PACK>
-__global__ __launch_bounds__(kThreads) void lowrank_shrink_kernel(LowRankArgs a, ShrinkJob jx,
+__global__ __launch_bounds__(kThreads, V * NR >= 8 ? 2 : 3) void lowrank_shrink_kernel(LowRankArgs a, ShrinkJob jx,
                                                                   ShrinkJob jy, int groups) {
   __shared__ f32x4 red[kWaves / 2 * NR * V * kWave];
   __shared__ TokenTile<16 * V> tile;
@@ -338,7 +403,7 @@ __global__ __launch_bounds__(kThreads) void lowrank_shrink_kernel(LowRankArgs a,
 // ranks (hi and lo of a 16-bit type, or fp32).
 __host__ __device__ inline int packed_row(int R) { return R <= 16 ? 64 : (R + 31) / 32 * 128; }
 
-constexpr int kPackTokens = 64;
+constexpr int kPackTokens = 32;  // small tiles: the launch is short and wants many workgroups
 
 // Adds the slices of u (or du) in order and writes them as the operands that
 // the later kernels load, so that the sum and the split into halves are made
@@ -359,7 +424,7 @@ __global__ __launch_bounds__(kThreads) void lowrank_pack_kernel(LowRankArgs a, i
     const int r = i / (TT / 4), t = i % (TT / 4) * 4;
     const float* p = u + (int64_t)r * a.Tp + t0 + t;
     f32x4 v = *(const f32x4*)p;
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 1; s < slices; ++s) v += *(const f32x4*)(p + s * size);
 #pragma unroll
     for (int e = 0; e < 4; ++e) us[r * LD + t + e] = v[e];
@@ -401,10 +466,10 @@ __global__ __launch_bounds__(kThreads) void lowrank_pack_kernel(LowRankArgs a, i
     }
   }
   if constexpr (BACKWARD) {
-    const int lane = tid % kWave;
+    const int lane = tid % TT;
     const int64_t t = t0 + lane;
     const int ad = __is_same(T, _Float16) && t < a.T ? a.tokad[t] : -1;
-    for (int r = tid / kWave; r < R; r += kWaves) {
+    for (int r = tid / TT; r < R; r += kThreads / TT) {
       float v = us[r * LD + lane];
       const int64_t at = (int64_t)r * a.Tp + t;
       if constexpr (sizeof(T) == 4) {
@@ -412,15 +477,15 @@ __global__ __launch_bounds__(kThreads) void lowrank_pack_kernel(LowRankArgs a, i
       } else {
         if constexpr (__is_same(T, _Float16)) {
           float big = 0.f;
-          uint64_t rest = __ballot(ad >= 0);
+          // both ranks of the wave hold the same tokens
+          uint32_t rest = (uint32_t)__ballot(ad >= 0);
           while (rest) {
-            const int l = __builtin_ctzll(rest);
-            const bool same = ad == __builtin_amdgcn_readlane(ad, l) && lane / 32 == l / 32;
+            const bool same = ad == __shfl(ad, __builtin_ctz(rest), kWave);
             float m = same ? fabsf(v) : 0.f;
 #pragma unroll
-            for (int o = 1; o < kWave; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
+            for (int o = 1; o < TT; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
             big = same ? m : big;
-            rest &= ~__ballot(same);
+            rest &= ~(uint32_t)__ballot(same);
           }
           const Pow2 p = pow2_of(big);
           v *= p.down;
@@ -573,6 +638,7 @@ struct TileAdapters {
   int tok[TT];
   int ad[TT];
   int rank[TT];
+  float up[TT];  // scale of the token's packed ranks (f16)
   int count;
 };
 
@@ -586,9 +652,10 @@ __device__ __forceinline__ void load_tokad(const LowRankArgs& a, int64_t t0, int
 
 // By all threads; ends with a barrier.
 template <int TT, int THREADS>
-__device__ __forceinline__ void tile_adapters(const LowRankArgs& a, int64_t t0,
+__device__ __forceinline__ void tile_adapters(const LowRankArgs& a, int64_t t0, bool scaled,
                                               TileAdapters<TT>& s) {
   load_tokad<TT, THREADS>(a, t0, s.tok);
+  if (scaled && threadIdx.x < TT) s.up[threadIdx.x] = a.up[t0 + threadIdx.x];
   __syncthreads();
   if (threadIdx.x < kWave) {
     AdapterWalk<TT> walk(s.tok);
@@ -612,70 +679,74 @@ __device__ __forceinline__ void tile_adapters(const LowRankArgs& a, int64_t t0,
 }
 
 // The tile's ranks as operands.  Column n of product q is the token V n + q,
-// so that a lane's V columns are neighbours in memory.  They come packed from
-// memory (PACKED) or from the fp32 rows staged in shared memory, and stay in
-// registers for up to STEPS K blocks (packed ones are loaded again where there
-// are more).
-template <typename T, int V, int STEPS, bool SMALL, bool PACKED>
-struct UOperand {
-  static constexpr int N = STEPS > 0 ? STEPS : 1;
-  Frag<T> hi[V][N], lo[V][N];
-  float up[V], down[V];
-  const char* row;
-  const float* us;
-  int row_bytes, width, blocks;
+// so that a lane's V columns are neighbours in memory.  Ranks up to 16 stay in
+// registers, one fragment a product; more of them would leave one wave a SIMD
+// (64 ranks: 128 registers, 145 us where shared memory takes
+// 97 us for 8192 tokens and 11008 rows), so they stay in shared memory as
+// pack wrote them, rows ordered by product for reads without bank conflicts.
+// A tile of single tokens (V = 1) has its ranks staged there as fp32 instead.
+template <int V>
+__host__ __device__ inline int operand_bytes(int R) {
+  return V == 1 ? 16 * staged_width(R) * 4 : R <= 16 ? 0 : 16 * V * (packed_row(R) + 16);
+}
 
-  __device__ __forceinline__ void get(int q, int k, Frag<T>& h, Frag<T>& l) const {
-    const int g = lane_id() / 16;
-    if constexpr (PACKED) {
-      const char* p = row + q * row_bytes;
-      if constexpr (SMALL)
-        __builtin_memcpy(&h, __builtin_assume_aligned(p + g * 16, 16), 16);
-      else if constexpr (sizeof(T) == 4)
-        __builtin_memcpy(&h, __builtin_assume_aligned(p + k * 128 + g * 32, 16), 32);
-      else {
-        __builtin_memcpy(&h, __builtin_assume_aligned(p + k * 128 + g * 16, 16), 16);
-        __builtin_memcpy(&l, __builtin_assume_aligned(p + k * 128 + 64 + g * 16, 16), 16);
-      }
-    } else {
-      h = u_frag<T, SMALL>(us + q * width, k, false, down[q]);
-      if constexpr (!SMALL && sizeof(T) == 2) l = u_frag<T, SMALL>(us + q * width, k, true, down[q]);
-    }
+template <int V, int THREADS>
+__device__ __forceinline__ void copy_rows(const LowRankArgs& a, int64_t t0, char* lds) {
+  const int row = packed_row(a.R), pieces = row / 16;
+  const char* from = (const char*)a.rows + t0 * row;
+  for (int i = threadIdx.x; i < 16 * V * pieces; i += THREADS) {
+    const int t = i / pieces, c = i % pieces;
+    __builtin_memcpy(__builtin_assume_aligned(lds + (t % V * 16 + t / V) * (row + 16) + c * 16, 16),
+                     __builtin_assume_aligned(from + (int64_t)i * 16, 16), 16);
   }
-  __device__ __forceinline__ UOperand(const LowRankArgs& a, int64_t t0, const float* staged) {
-    const int n = lane_id() % 16;
+}
+
+template <typename T, int V, bool SMALL>
+struct UOperand {
+  Frag<T> reg[SMALL ? V : 1];
+  float up, down;  // of staged ranks
+  const char* lds;
+  int row, blocks;
+
+  __device__ __forceinline__ UOperand(const LowRankArgs& a, int64_t t0, const char* staged) {
+    const int n = lane_id() % 16, g = lane_id() / 16;
     blocks = SMALL ? 1 : (a.R + 31) / 32;
-    row_bytes = packed_row(a.R);
-    width = staged_width(a.R);
-    row = (const char*)a.rows + (t0 + n * V) * row_bytes;
-    us = staged + n * V * width;
+    row = V == 1 ? staged_width(a.R) * 4 : packed_row(a.R) + 16;
+    lds = staged + n * row;
+    up = down = 1.f;
+    if constexpr (V == 1) {
+      const Pow2 p = row_pow2<T>((const float*)lds, a.R);
+      up = p.up;
+      down = p.down;
+      if constexpr (SMALL) reg[0] = u_frag<T, true>((const float*)lds, 0, false, down);
+    } else if constexpr (SMALL) {
 #pragma unroll
-    for (int q = 0; q < V; ++q) {
-      up[q] = down[q] = 1.f;
-      if constexpr (__is_same(T, _Float16)) {
-        if constexpr (PACKED) {
-          up[q] = a.up[t0 + n * V + q];
-        } else {
-          const Pow2 p = row_pow2<T>(us + q * width, a.R);
-          up[q] = p.up;
-          down[q] = p.down;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < STEPS; ++k) get(q, k, hi[q][k], lo[q][k]);
+      for (int q = 0; q < V; ++q)
+        __builtin_memcpy(&reg[q],
+                         __builtin_assume_aligned((const char*)a.rows + (t0 + n * V + q) * 64 + g * 16, 16),
+                         16);
     }
   }
   // acc[q] += f u_q for block k (not yet scaled by up)
   __device__ __forceinline__ void product(int k, const Frag<T>& f, f32x4 (&acc)[V]) const {
+    const int g = lane_id() / 16;
 #pragma unroll
     for (int q = 0; q < V; ++q) {
-      if constexpr (STEPS > 0) {
-        acc[q] = u_mma<T, SMALL>(f, hi[q][k], lo[q][k], acc[q]);
+      Frag<T> h, l;
+      if constexpr (SMALL) {
+        h = l = reg[q];
+      } else if constexpr (V == 1) {
+        h = u_frag<T, false>((const float*)lds, k, false, down);
+        l = u_frag<T, false>((const float*)lds, k, true, down);
       } else {
-        Frag<T> h, l;
-        get(q, k, h, l);
-        acc[q] = u_mma<T, SMALL>(f, h, l, acc[q]);
+        const char* p = lds + q * 16 * row + k * 128 + g * (int)sizeof(h);
+        __builtin_memcpy(&h, __builtin_assume_aligned(p, 16), sizeof(h));
+        if constexpr (sizeof(T) == 2)
+          __builtin_memcpy(&l, __builtin_assume_aligned(p + 64, 16), sizeof(l));
+        else
+          l = h;
       }
+      acc[q] = u_mma<T, SMALL>(f, h, l, acc[q]);
     }
   }
 };
@@ -708,19 +779,16 @@ __device__ __forceinline__ void load_rows(const T* p, int64_t ld, int64_t ob, in
 // next rows' values and factors are requested before the present ones are
 // used.  Distinct adapters are computed for the whole tile one after another
 // (D at a time in flight) and selected per token.
-template <typename T, int V, int STEPS, bool SMALL, bool PACKED, bool DX>
+template <typename T, int V, int STEPS, bool SMALL, bool DX>
 __device__ __forceinline__ void stream_rows(const LowRankArgs& a, const TileAdapters<16 * V>& tile,
-                                            const float* staged, int64_t t0, int64_t row0,
+                                            const char* staged, int64_t t0, int64_t row0,
                                             int64_t row_end) {
   constexpr int D = V == 1 ? 4 : 1, N = STEPS > 0 ? STEPS : 1;
   const int lane = lane_id(), n = lane % 16, wave = threadIdx.x / kWave;
-  const UOperand<T, V, STEPS, SMALL, PACKED> u(a, t0, staged);
+  const UOperand<T, V, SMALL> u(a, t0, staged);
   const int64_t rows = DX ? a.n_in : a.n_out, t = t0 + n * V;
   const int cnt = clampi(a.T - t, 0, V);
   const int count = __builtin_amdgcn_readfirstlane(tile.count);
-  int ra[V];
-#pragma unroll
-  for (int q = 0; q < V; ++q) ra[q] = tile.tok[n * V + q];
   const T* y = (const T*)a.y;
   T* out = (T*)a.out;
   auto factor = [&](int c, int64_t ob, int k) {
@@ -776,6 +844,9 @@ __device__ __forceinline__ void stream_rows(const LowRankArgs& a, const TileAdap
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         if (d > 0 && c0 + d >= count) break;
+        // what is in shared memory is not to be kept in registers over the
+        // loops (or one wave a SIMD is left)
+        asm volatile("" ::: "memory");
         const int ad = __builtin_amdgcn_readfirstlane(tile.ad[c0 + d]);
         f32x4 acc[V];
 #pragma unroll
@@ -787,12 +858,15 @@ __device__ __forceinline__ void stream_rows(const LowRankArgs& a, const TileAdap
           for (int k = 0; k < u.blocks; ++k) u.product(k, factor(c0 + d, ob, k), acc);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int q = 0; q < V; ++q) {
+          const bool mine = tile.tok[n * V + q] == ad;
+          const float up = !__is_same(T, _Float16) ? 1.f : V == 1 ? u.up : tile.up[n * V + q];
 #pragma unroll
-          for (int q = 0; q < V; ++q) {
-            const float w = __is_same(T, _Float16) ? acc[q][i] * u.up[q] : acc[q][i];
-            v[i][q] = ra[q] != ad ? v[i][q] : DX ? w : v[i][q] + w;
+          for (int i = 0; i < 4; ++i) {
+            const float w = __is_same(T, _Float16) ? acc[q][i] * up : acc[q][i];
+            v[i][q] = !mine ? v[i][q] : DX ? w : v[i][q] + w;
           }
+        }
       }
     }
 #pragma unroll
@@ -806,17 +880,20 @@ __device__ __forceinline__ void stream_rows(const LowRankArgs& a, const TileAdap
 // Token tiles are the fastest index, so that neighbouring workgroups stream
 // neighbouring parts of the same rows.
 template <typename T, int V, int STEPS, bool SMALL>
-__global__ __launch_bounds__(kThreads) void lowrank_expand_kernel(LowRankArgs a, int slices,
+__global__ __launch_bounds__(kThreads, 3) void lowrank_expand_kernel(LowRankArgs a, int slices,
                                                                   int tiles, int rows_per_block) {
   constexpr int TT = 16 * V;
-  extern __shared__ float us[];
+  extern __shared__ __attribute__((aligned(16))) char operand[];
   __shared__ TileAdapters<TT> tile;
   const uint32_t b = xcd_chunk(blockIdx.x, gridDim.x);
   const int64_t t0 = (int64_t)(b % tiles) * TT, row0 = (int64_t)(b / tiles) * rows_per_block;
   const int64_t end = row0 + rows_per_block < a.n_out ? row0 + rows_per_block : a.n_out;
-  if constexpr (V == 1) stage_u<TT, kThreads>(a, a.u, slices, t0, us);
-  tile_adapters<TT, kThreads>(a, t0, tile);
-  stream_rows<T, V, STEPS, SMALL, V != 1, false>(a, tile, us, t0, row0, end);
+  if constexpr (V == 1)
+    stage_u<TT, kThreads>(a, a.u, slices, t0, (float*)operand);
+  else if constexpr (!SMALL)
+    copy_rows<V, kThreads>(a, t0, operand);
+  tile_adapters<TT, kThreads>(a, t0, __is_same(T, _Float16) && V != 1, tile);
+  stream_rows<T, V, STEPS, SMALL, false>(a, tile, operand, t0, row0, end);
 }
 
 // ------------------------------------------------------------------ outer --
@@ -985,10 +1062,11 @@ __device__ __forceinline__ void outer_tile(const LowRankArgs& a, bool is_x, int6
 // dA, dB and dx in one launch: they need the same packed ranks and nothing of
 // each other, and the reads of the first two go beside the writes of the last.
 template <typename T, int NR, int STEPS, bool SMALL>
-__global__ __launch_bounds__(kThreads) void lowrank_gradients_kernel(LowRankArgs a, int xblocks,
+__global__ __launch_bounds__(kThreads, 3) void lowrank_gradients_kernel(LowRankArgs a, int xblocks,
                                                                      int yblocks, int tiles,
                                                                      int rows_per_block) {
   constexpr int V = 16 / sizeof(T), TT = 16 * V, FF = kOuterFeatures;
+  extern __shared__ __attribute__((aligned(16))) char operand[];
   __shared__ union {
     OuterShared<FF, NR> outer;
     TileAdapters<TT> tile;
@@ -1003,8 +1081,9 @@ __global__ __launch_bounds__(kThreads) void lowrank_gradients_kernel(LowRankArgs
   } else {
     const int64_t b = xcd_chunk(blockIdx.x - outer, gridDim.x - outer), t0 = b % tiles * TT, row0 = b / tiles * rows_per_block;
     const int64_t end = row0 + rows_per_block < a.n_in ? row0 + rows_per_block : a.n_in;
-    tile_adapters<TT, kThreads>(a, t0, sh.tile);
-    stream_rows<T, V, STEPS, SMALL, true, true>(a, sh.tile, nullptr, t0, row0, end);
+    if constexpr (!SMALL) copy_rows<V, kThreads>(a, t0, operand);
+    tile_adapters<TT, kThreads>(a, t0, __is_same(T, _Float16), sh.tile);
+    stream_rows<T, V, STEPS, SMALL, true>(a, sh.tile, operand, t0, row0, end);
   }
 }
 
@@ -1120,26 +1199,35 @@ __global__ __launch_bounds__(kProjectThreads) void lowrank_project_kernel(LowRan
 // --------------------------------------------------------------- launches --
 
 constexpr int64_t kFillBlocks = 512;  // two workgroups on each of the 256 CUs
+// Busy workgroups of the shrink kernel.  More of them mean more partial sums
+// (8192 tokens, 16 ranks: 25 us at 256, 27 at 384, 32 at 1024), fewer leave
+// tiles of several adapters behind (2047 tokens of 23 requests, both products:
+// 54 us at 256, 41 at 384, 48 at 512).
+constexpr int64_t kShrinkBlocks = 384;
 
-// Tokens a lane holds of a row in the shrink kernel.
-int token_width(int op, int dtype, int64_t T) {
-  const int most = op == kLowRankProject ? 4 : dtype == kF32 ? 4 : 8;
+// Tokens a lane holds of a row in the shrink kernel: 16 bytes a load where the
+// sums' registers leave four waves a SIMD.
+int token_width(int op, int dtype, int64_t T, int64_t R) {
+  const int most = op == kLowRankProject || dtype == kF32 || R > 32 ? 4 : 8;
   int v = 1;
   while (v < most && T > 16 * v) v *= 2;
   return v;
 }
 
 // Distinct adapters that share a tile are spread over this many workgroups:
-// the tile's mean number of requests, at most the adapters there are.
-int adapter_groups(int64_t T, int64_t S, int64_t n, int64_t tile) {
-  const int64_t t = T < tile ? T : tile;
-  int64_t g = S * t / (T > 0 ? T : 1);
+// one more than the mean number of requests that start in a tile, for the one
+// that reaches into it.  Where few tiles have a second adapter, those take
+// twice the time instead of every tile an idle workgroup.
+int adapter_groups(double mean, int64_t S, int64_t n) {
+  if (mean < 0.25) return 1;
+  int64_t g = (int64_t)mean + 2;
   g = g < n ? g : n;
+  g = g < S ? g : S;
   return (int)(g < 1 ? 1 : g > 64 ? 64 : g);
 }
 
-int slices_for(int64_t blocks, int64_t K) {
-  int64_t s = cdiv(kFillBlocks, blocks > 0 ? blocks : 1);
+int slices_for(double blocks, int64_t K) {
+  int64_t s = (int64_t)(kShrinkBlocks / blocks);
   const int64_t most = cdiv(K, 32) / (2 * kWaves);  // two steps a wave at least
   s = s < most ? s : most;
   return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
@@ -1152,17 +1240,15 @@ hipError_t shrink_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s)
   ShrinkJob jy{a.y, a.B, a.du, a.ldy, a.n_out, l.slices_du};
   const dim3 grid((unsigned)(cdiv(a.T, 16 * V) * l.groups * rcs *
                              (l.slices_u + (BACKWARD ? l.slices_du : 0))));
-  const int nr = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4;
-  if (nr == 1)
-    hipLaunchKernelGGL((lowrank_shrink_kernel<T, V, 1, BACKWARD, PACK>), grid, dim3(kThreads), 0, s,
-                       a, jx, jy, l.groups);
-  else if (nr == 2)
-    hipLaunchKernelGGL((lowrank_shrink_kernel<T, V, 2, BACKWARD, PACK>), grid, dim3(kThreads), 0, s,
-                       a, jx, jy, l.groups);
-  else
-    hipLaunchKernelGGL((lowrank_shrink_kernel<T, V, 4, BACKWARD, PACK>), grid, dim3(kThreads), 0, s,
-                       a, jx, jy, l.groups);
-  return hipGetLastError();
+  auto launch = [&](auto ranks) {
+    hipLaunchKernelGGL((lowrank_shrink_kernel<T, V, decltype(ranks)::value, BACKWARD, PACK>), grid,
+                       dim3(kThreads), 0, s, a, jx, jy, l.groups);
+    return hipGetLastError();
+  };
+  if (a.R <= 16) return launch(Int<1>{});
+  if (a.R <= 32) return launch(Int<2>{});
+  if constexpr (V <= 4) return launch(Int<4>{});
+  return hipErrorInvalidValue;  // token_width keeps such tiles narrow
 }
 
 template <typename T, bool BACKWARD, bool PACK>
@@ -1205,7 +1291,7 @@ template <typename T, int V>
 hipError_t expand_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
   const int64_t tiles = cdiv(a.T, 16 * V), per = rows_per_block(a.n_out, tiles);
   const dim3 grid((unsigned)(cdiv(a.n_out, per) * tiles));
-  const size_t lds = V == 1 ? staged_bytes(16, a.R) : 0;
+  const size_t lds = operand_bytes<V>(a.R);
   if (a.R <= 16)
     hipLaunchKernelGGL((lowrank_expand_kernel<T, V, 1, true>), grid, dim3(kThreads), lds, s, a,
                        l.slices_u, (int)tiles, (int)per);
@@ -1227,18 +1313,19 @@ hipError_t gradients(const LowRankArgs& a, hipStream_t s) {
   const int64_t xb = cdiv(a.n_in, 16 * kOuterFeatures), yb = cdiv(a.n_out, 16 * kOuterFeatures);
   const int64_t tiles = cdiv(a.T, TT), per = rows_per_block(a.n_in, tiles > 0 ? tiles : 1);
   const dim3 grid((unsigned)((xb + yb) * a.n * cdiv(a.R, 64) + cdiv(a.n_in, per) * tiles));
+  const size_t lds = operand_bytes<16 / sizeof(T)>(a.R);
   const int t = (int)(tiles > 0 ? tiles : 1);
   if (a.R <= 16)
-    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 1, 1, true>), grid, dim3(kThreads), 0, s, a,
+    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 1, 1, true>), grid, dim3(kThreads), lds, s, a,
                        (int)xb, (int)yb, t, (int)per);
   else if (a.R <= 32)
-    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 2, 1, false>), grid, dim3(kThreads), 0, s, a,
+    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 2, 1, false>), grid, dim3(kThreads), lds, s, a,
                        (int)xb, (int)yb, t, (int)per);
   else if (a.R <= 64)
-    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 4, 2, false>), grid, dim3(kThreads), 0, s, a,
+    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 4, 2, false>), grid, dim3(kThreads), lds, s, a,
                        (int)xb, (int)yb, t, (int)per);
   else
-    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 4, 0, false>), grid, dim3(kThreads), 0, s, a,
+    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 4, 0, false>), grid, dim3(kThreads), lds, s, a,
                        (int)xb, (int)yb, t, (int)per);
   return hipGetLastError();
 }
@@ -1294,10 +1381,13 @@ LowRankLayout lowrank_layout(int op, int dtype, int64_t T, int64_t S, int64_t n,
   LowRankLayout l{};
   const int64_t eb = dtype == kF32 ? 4 : 2;
   l.Tp = cdiv(T, 128) * 128;  // whole tiles
-  l.width = token_width(op, dtype, T);
-  l.groups = adapter_groups(T, S, n, 16 * l.width);
+  l.width = token_width(op, dtype, T, R);
   const int64_t tiles = cdiv(T, 16 * l.width);
-  const int64_t blocks = tiles * l.groups * cdiv(R, 64) * (op == kLowRankBackward ? 2 : 1);
+  const double mean = (double)S / (double)(tiles > 0 ? tiles : 1);
+  l.groups = adapter_groups(mean, S, n);
+  // busy workgroups: an adapter in the mean, or each request that starts
+  const double busy = mean < 1 ? 1 : mean < l.groups ? mean : l.groups;
+  const double blocks = (double)tiles * busy * (double)cdiv(R, 64) * (op == kLowRankBackward ? 2 : 1);
   l.slices_u = slices_for(blocks, n_in);
   l.slices_du = op == kLowRankBackward ? slices_for(blocks, n_out) : 0;
   size_t at = 0;
