@@ -944,7 +944,8 @@ spops_status low_rank_args(const spops_low_rank* L, int op, const void* second, 
     if (!second || !xt || !out) return SPOPS_ERR_NULL;
     const LowRankLayout l = lowrank_layout(op, L->dtype, L->tokens, L->requests, L->adapters,
                                            L->rank, L->in_features, L->out_features);
-    if (!workspace || bytes < l.bytes || ((uintptr_t)workspace & 255)) return SPOPS_ERR_WORKSPACE;
+    if (l.bytes > 0 && (!workspace || bytes < l.bytes || ((uintptr_t)workspace & 255)))
+      return SPOPS_ERR_WORKSPACE;
   }
   a.T = L->tokens;
   a.n_in = L->in_features;

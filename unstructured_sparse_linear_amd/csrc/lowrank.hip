@@ -23,7 +23,8 @@
 //   expand   y + B u
 //   gradients  dA and dB, one workgroup per adapter and 32 features, and
 //            dx = A^T du
-//   project  W x + B u on few tokens
+//   project  W x + B u on the tokens of a decode step
+//   few      either forward on a few tokens in one launch
 // Requests meet the tiles only through each token's adapter, which the shrink
 // kernel finds and writes once.  A tile whose tokens have several adapters is
 // computed once per distinct adapter and the results selected per token (never
@@ -1089,109 +1090,321 @@ __global__ __launch_bounds__(kThreads, 3) void lowrank_gradients_kernel(LowRankA
 
 // ---------------------------------------------------------------- project --
 
-// y = W x + B u on a tile of 16 V tokens: a workgroup takes 16 MO rows of W,
-// its waves a slice of the features each; x comes as the fragments that the
-// shrink kernel packed.  The waves' sums meet in shared memory, where the
-// adapters' part is added.
-template <typename T, int V, int MO, bool SMALL>
-__global__ __launch_bounds__(kProjectThreads) void lowrank_project_kernel(LowRankArgs a, int slices,
-                                                                        int row_blocks) {
-  constexpr int TT = 16 * V;
+// y = W x + B u on a tile of 16 V tokens: a workgroup takes 16 rows of W, eight
+// waves a slice of the features each; x comes as the fragments that the shrink
+// kernel packed.  V more waves make the adapters' part of 16 tokens each
+// meanwhile: their chain of dependent loads (u, adapter, B) is as long as the
+// stream of W and would double the time behind it.  All meet in shared memory.
+template <typename T, int V, bool SMALL>
+__global__ __launch_bounds__((kProjectWaves + V) * kWave) void lowrank_project_kernel(
+    LowRankArgs a, int slices, int row_blocks) {
+  constexpr int TT = 16 * V, D = 4;
   extern __shared__ float us[];
-  __shared__ f32x4 red[kProjectWaves * MO * V * kWave];
-  __shared__ int tok[TT];
-  const int lane = lane_id(), n = lane % 16, g = lane / 16, wave = threadIdx.x / kWave;
+  __shared__ f32x4 red[(kProjectWaves + 1) * V * kWave];
+  const int lane = lane_id(), n = lane % 16, g = lane / 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int block = blockIdx.x % row_blocks;
   const int64_t tile = blockIdx.x / row_blocks;
   int64_t t0 = tile * TT;
   if (t0 > a.T - TT) t0 = a.T > TT ? a.T - TT : 0;
-  load_tokad<TT, kProjectThreads>(a, t0, tok);
-  stage_u<TT, kProjectThreads>(a, a.u, slices, t0, us);
-  const int64_t steps = cdiv(a.n_in, 32);
-  const int64_t s0 = steps * wave / kProjectWaves, s1 = steps * (wave + 1) / kProjectWaves;
-  const int64_t o0 = (int64_t)block * (16 * MO);
-  const T* w[MO];
-#pragma unroll
-  for (int k = 0; k < MO; ++k) {
-    const int64_t o = o0 + k * 16 + n;
-    w[k] = (const T*)a.W + (o < a.n_out ? o : a.n_out - 1) * a.ldw;
-  }
-  const T* xp = (const T*)a.packed + (tile * steps * V * kWave + lane) * 8;
-  f32x4 acc[MO * V];
-#pragma unroll
-  for (int k = 0; k < MO * V; ++k) acc[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int64_t whole = a.n_in / 32 < s1 ? a.n_in / 32 : s1;
-  // U steps' loads are issued together: a wave alone keeps U (MO + V) KB (f16)
-  // in flight, and the eight waves of a workgroup cover the latency of HBM
-  constexpr int U = 8 / V;
-  auto run = [&](int64_t at, auto steps_together) {
-    constexpr int N = decltype(steps_together)::value;
-    Frag<T> fw[N][MO], fx[N][V];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-#pragma unroll
-      for (int k = 0; k < MO; ++k) fw[i][k] = load8(w[k] + (at + i) * 32 + g * 8);
-#pragma unroll
-      for (int j = 0; j < V; ++j) fx[i][j] = load8(xp + ((at + i) * V + j) * kWave * 8);
-    }
-    __builtin_amdgcn_sched_barrier(0);  // or the loads are spread among the products
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int k = 0; k < MO; ++k)
-#pragma unroll
-        for (int j = 0; j < V; ++j) acc[k * V + j] = mma(fx[i][j], fw[i][k], acc[k * V + j]);
+  const int64_t lim = a.T - V, o0 = (int64_t)block * 16;
+  const int64_t o = o0 + n, oc = o < a.n_out ? o : a.n_out - 1;
+  // token of row m of tile j
+  auto token = [&](int m, int j) {
+    const int64_t t = t0 + m * V;
+    return (t < lim ? t : lim) + j;
   };
-  int64_t s = s0;
-  for (; s + U <= whole; s += U) run(s, Int<U>{});
-  for (; s < whole; ++s) run(s, Int<1>{});
-  if (s < s1) {
-    const int cnt = clampi(a.n_in - s * 32 - g * 8, 0, 8);
+  if (wave < kProjectWaves) {
+    const int64_t steps = cdiv(a.n_in, 32);
+    const int64_t s0 = steps * wave / kProjectWaves, s1 = steps * (wave + 1) / kProjectWaves;
+    const T* w = (const T*)a.W + oc * a.ldw + g * 8;
+    const T* xp = (const T*)a.packed + (tile * steps * V * kWave + lane) * 8;
+    f32x4 acc[V];
 #pragma unroll
-    for (int k = 0; k < MO; ++k) {
-      const Frag<T> fw = load8_count(w[k] + s * 32 + g * 8, cnt);
+    for (int j = 0; j < V; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int64_t whole = a.n_in / 32 < s1 ? a.n_in / 32 : s1;
+    // U steps' loads are issued together
+    constexpr int U = 8 / V;
+    auto run = [&](int64_t at, auto steps_together) {
+      constexpr int N = decltype(steps_together)::value;
+      Frag<T> fw[N], fx[N][V];
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        acc[k * V + j] = mma(load8(xp + (s * V + j) * kWave * 8), fw, acc[k * V + j]);
-    }
-  }
+      for (int i = 0; i < N; ++i) {
+        fw[i] = load8(w + (at + i) * 32);
 #pragma unroll
-  for (int k = 0; k < MO * V; ++k) red[(wave * MO * V + k) * kWave + lane] = acc[k];
-  __syncthreads();
-  const int64_t lim = a.T - V;
-  const int blocks = SMALL ? 1 : (a.R + 31) / 32;
-  for (int k = wave; k < MO * V; k += kProjectWaves) {
-    f32x4 v = red[k * kWave + lane];
+        for (int j = 0; j < V; ++j) fx[i][j] = load8(xp + ((at + i) * V + j) * kWave * 8);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // or the loads are spread among the products
 #pragma unroll
-    for (int h = 1; h < kProjectWaves; ++h) v += red[(h * MO * V + k) * kWave + lane];
-    const int j = k % V;
-    const int64_t o = o0 + k / V * 16 + n, oc = o < a.n_out ? o : a.n_out - 1;
-    auto local = [&](int m) {
-      const int64_t t = t0 + m * V;
-      return (int)((t < lim ? t : lim) - t0) + j;
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = mma(fx[i][j], fw[i], acc[j]);
     };
-    const float* row = us + local(n) * staged_width(a.R);
+    int64_t s = s0;
+#pragma unroll 1
+    for (; s + U <= whole; s += U) run(s, Int<U>{});
+#pragma unroll 1
+    for (; s < whole; ++s) run(s, Int<1>{});
+    if (s < s1) {
+      const Frag<T> fw = load8_count(w + s * 32, clampi(a.n_in - s * 32 - g * 8, 0, 8));
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] = mma(load8(xp + (s * V + j) * kWave * 8), fw, acc[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) red[(wave * V + j) * kWave + lane] = acc[j];
+  } else {
+    const int j = wave - kProjectWaves, rs = staged_width(a.R);
+    float* mine = us + j * 16 * rs;
+    const int64_t tn = token(n, j);
+    int ad_n = tn < a.T ? a.tokad[tn] : -1;
+    ad_n = ad_n < a.n ? ad_n : -1;
+    for (int r = g; r < rs - 4; r += 4) {
+      float v = 0.f;
+      if (r < a.R) {
+        const float* p = a.u + (int64_t)r * a.Tp + tn;
+#pragma unroll 4
+        for (int s = 0; s < slices; ++s) v += p[(int64_t)s * a.R * a.Tp];
+      }
+      mine[n * rs + r] = v;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the wave alone reads its ranks
+    __builtin_amdgcn_wave_barrier();
+    const float* row = mine + n * rs;
     const Pow2 p = row_pow2<T>(row, a.R);
-    AdapterWalk<TT> walk(tok);
-    int ad;
-    while (walk.next(ad)) {
-      const int rank = rank_of(a, ad);
-      f32x4 c = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int b = 0; b < blocks; ++b) {
-        const Frag<T> hi = u_frag<T, SMALL>(row, b, false, p.down);
-        const Frag<T> lo = u_frag<T, SMALL>(row, b, true, p.down);
-        c = token_mma<T, SMALL>(hi, lo, b_frag<T, SMALL>(a, ad, oc, rank, b), c);
+    const int blocks = SMALL ? 1 : (a.R + 31) / 32;
+    int ra[4];
+    float up[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ra[i] = __shfl(ad_n, g * 4 + i, kWave);
+      up[i] = __is_same(T, _Float16) ? __shfl(p.up, g * 4 + i, kWave) : 1.f;
+    }
+    f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+    uint64_t rest = __ballot(ad_n >= 0);
+    while (rest) {
+      // D distinct adapters, their factors requested together
+      int ads[D], count = 0;
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        ads[d] = d > 0 ? ads[d - 1] : 0;
+        if (rest) {
+          ads[d] = __builtin_amdgcn_readlane(ad_n, __builtin_ctzll(rest));
+          rest &= ~__ballot(ad_n == ads[d]);
+          ++count;
+        }
+      }
+      f32x4 c[D];
+#pragma unroll
+      for (int d = 0; d < D; ++d) c[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < blocks; ++k) {
+        const Frag<T> hi = u_frag<T, SMALL>(row, k, false, p.down);
+        const Frag<T> lo = u_frag<T, SMALL>(row, k, true, p.down);
+        Frag<T> f[D];
+#pragma unroll
+        for (int d = 0; d < D; ++d) f[d] = b_frag<T, SMALL>(a, ads[d], oc, rank_of(a, ads[d]), k);
+#pragma unroll
+        for (int d = 0; d < D; ++d) c[d] = token_mma<T, SMALL>(hi, lo, f[d], c[d]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float up = __is_same(T, _Float16) ? __shfl(p.up, g * 4 + i, kWave) : 1.f;
-        v[i] = tok[local(g * 4 + i)] == ad ? v[i] + c[i] * up : v[i];
-      }
+      for (int d = 0; d < D; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = d < count && ra[i] == ads[d] ? c[d][i] * up[i] : v[i];
     }
+    red[(kProjectWaves * V + j) * kWave + lane] = v;
+  }
+  __syncthreads();
+  if (wave < V) {
+    f32x4 v = red[wave * kWave + lane];
+#pragma unroll
+    for (int h = 1; h < kProjectWaves; ++h) v += red[(h * V + wave) * kWave + lane];
+    const f32x4 add = red[(kProjectWaves * V + wave) * kWave + lane];
     if (o < a.n_out) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        store_bits((T*)a.out + o * a.ldo + t0 + local(g * 4 + i), out_bits(v[i], (T*)nullptr));
+      for (int i = 0; i < 4; ++i) {
+        const int64_t t = token(g * 4 + i, wave);
+        if (t < a.T) store_bits((T*)a.out + o * a.ldo + t, out_bits(v[i] + add[i], (T*)nullptr));
+      }
+    }
+  }
+}
+
+// -------------------------------------------------------------------- few --
+
+constexpr int kFewTokens = 16;
+
+// A few tokens with one adapter or two in one launch: every workgroup makes
+// u = A x for itself (from its XCD's L2, 128 KB for 16 ranks of 4096 features)
+// and then its rows: 16 of W and B (PROJECT: the waves split the features of
+// both W and A), or 128 of B (added to y).  Two launches cost more than the
+// repeated reads as long as a workgroup's share of A is no longer than twice
+// its rows of W: the rule below.
+template <typename T, bool PROJECT, int NR>
+__global__ __launch_bounds__(kProjectThreads) void lowrank_few_kernel(LowRankArgs a) {
+  constexpr bool SMALL = NR == 1;
+  constexpr int U = 4;
+  extern __shared__ float us[];
+  __shared__ f32x4 red[kProjectWaves * (NR > 1 ? NR : 1) * kWave];
+  __shared__ TokenTile<kFewTokens> tile;
+  const int lane = lane_id(), n = lane % 16, g = lane / 16;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t K = a.n_in, steps = cdiv(K, 32);
+  const int64_t s0 = steps * wave / kProjectWaves, s1 = steps * (wave + 1) / kProjectWaves;
+  const int64_t whole = K / 32 < s1 ? K / 32 : s1;
+  const int tok = n < a.T ? n : (int)a.T - 1, rs = staged_width(a.R);
+  const T* x = (const T*)a.x + tok;
+  const bool neighbours = a.ldx == 1;  // one token: the features lie together
+  auto x_frag = [&](int64_t k0) {
+    uint32_t b[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) b[s] = raw_bits(x + (k0 + s) * a.ldx);
+    Frag<T> f;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      if (sizeof(T) == 4)
+        f.w[s] = b[s];
+      else if (s % 2 == 0)
+        f.w[s / 2] = b[s] | b[s + 1] << 16;
+    }
+    return f;
+  };
+  auto x_tail = [&](int64_t k0) {
+    uint32_t b[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) b[s] = k0 + s < K ? raw_bits(x + (k0 + s) * a.ldx) : 0u;
+    Frag<T> f;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      if (sizeof(T) == 4)
+        f.w[s] = b[s];
+      else if (s % 2 == 0)
+        f.w[s / 2] = b[s] | b[s + 1] << 16;
+    }
+    return f;
+  };
+  // rows of M matrices of row length K against x, over this wave's features
+  auto dots = [&](auto count, const T* const* rows, f32x4* acc) {
+    constexpr int M = decltype(count)::value;
+    int64_t s = s0;
+    auto run = [&](auto together, auto near) {
+      constexpr int N = decltype(together)::value;
+      Frag<T> f[N][M], fx[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int64_t k0 = (s + i) * 32 + g * 8;
+#pragma unroll
+        for (int m = 0; m < M; ++m) f[i][m] = load8(rows[m] + k0);
+        if constexpr (decltype(near)::value)
+          fx[i] = load8(x + k0);
+        else
+          fx[i] = x_frag(k0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int m = 0; m < M; ++m) acc[m] = mma(f[i][m], fx[i], acc[m]);
+      s += N;
+    };
+    if (neighbours) {
+#pragma unroll 1
+      while (s + U <= whole) run(Int<U>{}, Int<1>{});
+    } else {
+#pragma unroll 1
+      while (s + 2 <= whole) run(Int<2>{}, Int<0>{});
+    }
+#pragma unroll 1
+    while (s < whole) run(Int<1>{}, Int<0>{});
+    if (s < s1) {
+      const int64_t k0 = s * 32 + g * 8;
+      const Frag<T> fx = x_tail(k0);
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        acc[m] = mma(load8_count(rows[m] + k0, clampi(K - k0, 0, 8)), fx, acc[m]);
+    }
+  };
+  const int64_t o0 = PROJECT ? (int64_t)blockIdx.x * 16
+                             : ((int64_t)blockIdx.x * kProjectWaves + wave) * 16;
+  const int64_t oc = o0 + n < a.n_out ? o0 + n : a.n_out - 1;
+  f32x4 accw[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
+  if constexpr (PROJECT) {
+    const T* rows[1] = {(const T*)a.W + oc * a.ldw};
+    dots(Int<1>{}, rows, accw);
+  }
+  for (int i = threadIdx.x; i < 16 * rs; i += kProjectThreads) us[i] = 0.f;
+  token_adapters<kFewTokens, kProjectThreads>(a, 0, tile);
+  // requested before u is made: the rows of y and of the first adapter's B
+  const bool rows_here = PROJECT ? wave == 0 : o0 < a.n_out;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (!PROJECT && rows_here && n < a.T) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = o0 + g * 4 + i;
+      if (r < a.n_out) v[i] = to_f32(((const T*)a.y)[r * a.ldy + n]);
+    }
+  }
+  AdapterWalk<kFewTokens> walk(tile.tok);
+  int ad, lead = -1;
+  Frag<T> fb{};
+  while (walk.next(ad)) {
+    if (lead < 0) {
+      lead = ad;
+      if (rows_here) fb = b_frag<T, SMALL>(a, ad, oc, rank_of(a, ad), 0);
+    }
+    f32x4 acc[NR];
+    const T* rows[NR];
+#pragma unroll
+    for (int q = 0; q < NR; ++q) {
+      const int r = q * 16 + n;
+      rows[q] = (const T*)a.A + ((int64_t)ad * a.R + (r < a.R ? r : a.R - 1)) * K;
+      acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    dots(Int<NR>{}, rows, acc);
+#pragma unroll
+    for (int q = 0; q < NR; ++q) red[(wave * NR + q) * kWave + lane] = acc[q];
+    __syncthreads();
+    if (wave < NR && n < a.T && tile.tok[n] == ad) {
+      f32x4 t = red[wave * kWave + lane];
+#pragma unroll
+      for (int h = 1; h < kProjectWaves; ++h) t += red[(h * NR + wave) * kWave + lane];
+      const float sc = a.scale ? a.scale[ad] : 1.f;
+      const int rank = rank_of(a, ad);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = wave * 16 + g * 4 + i;
+        if (r < rank) us[n * rs + r] = t[i] * sc;
+      }
+    }
+    __syncthreads();
+  }
+  if constexpr (PROJECT) {
+    red[wave * kWave + lane] = accw[0];
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+      for (int h = 1; h < kProjectWaves; ++h) accw[0] += red[h * kWave + lane];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = accw[0][i];
+    }
+  }
+  if (!rows_here) return;
+  const float* row = us + n * rs;
+  const Pow2 p = row_pow2<T>(row, a.R);
+  const Frag<T> hi = u_frag<T, SMALL>(row, 0, false, p.down);
+  const Frag<T> lo = u_frag<T, SMALL>(row, 0, true, p.down);
+  AdapterWalk<kFewTokens> again(tile.tok);
+  while (again.next(ad)) {
+    if (ad != lead) fb = b_frag<T, SMALL>(a, ad, oc, rank_of(a, ad), 0);
+    const f32x4 c = u_mma<T, SMALL>(fb, hi, lo, f32x4{0.f, 0.f, 0.f, 0.f});
+    if (tile.tok[n] == ad) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += c[i] * p.up;
+    }
+  }
+  if (n < a.T) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = o0 + g * 4 + i;
+      if (r < a.n_out) store_bits((T*)a.out + r * a.ldo + n, out_bits(v[i], (T*)nullptr));
     }
   }
 }
@@ -1330,22 +1543,42 @@ hipError_t gradients(const LowRankArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int V, int MO>
+template <typename T, int V>
 hipError_t project_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
-  const int64_t rb = cdiv(a.n_out, 16 * MO);
-  const dim3 grid((unsigned)(rb * cdiv(a.T, 16 * V)));
+  const int64_t rb = cdiv(a.n_out, 16);
+  const dim3 grid((unsigned)(rb * cdiv(a.T, 16 * V))), block((kProjectWaves + V) * kWave);
   const size_t lds = staged_bytes(16 * V, a.R);
   if (a.R <= 16)
-    hipLaunchKernelGGL((lowrank_project_kernel<T, V, MO, true>), grid, dim3(kProjectThreads), lds, s,
-                       a, l.slices_u, (int)rb);
+    hipLaunchKernelGGL((lowrank_project_kernel<T, V, true>), grid, block, lds, s, a, l.slices_u,
+                       (int)rb);
   else
-    hipLaunchKernelGGL((lowrank_project_kernel<T, V, MO, false>), grid, dim3(kProjectThreads), lds, s,
-                       a, l.slices_u, (int)rb);
+    hipLaunchKernelGGL((lowrank_project_kernel<T, V, false>), grid, block, lds, s, a, l.slices_u,
+                       (int)rb);
+  return hipGetLastError();
+}
+
+// One launch for up to 16 tokens where their distinct adapters cannot have
+// more than 32 ranks together.
+bool few(int op, int64_t T, int64_t S, int64_t n, int64_t R) {
+  int64_t distinct = S < T ? S : T;
+  distinct = distinct < n ? distinct : n;
+  return op != kLowRankBackward && T <= kFewTokens && R <= 32 && distinct * R <= 32;
+}
+
+template <typename T, bool PROJECT>
+hipError_t few_t(const LowRankArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)cdiv(a.n_out, PROJECT ? 16 : 16 * kProjectWaves));
+  const size_t lds = staged_bytes(16, a.R);
+  if (a.R <= 16)
+    hipLaunchKernelGGL((lowrank_few_kernel<T, PROJECT, 1>), grid, dim3(kProjectThreads), lds, s, a);
+  else
+    hipLaunchKernelGGL((lowrank_few_kernel<T, PROJECT, 2>), grid, dim3(kProjectThreads), lds, s, a);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t add_t(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
+  if (few(kLowRankAdd, a.T, a.S, a.n, a.R)) return few_t<T, false>(a, s);
   hipError_t e = shrink<T, false, false>(a, l, s);
   if (e != hipSuccess) return e;
   if (!packs(kLowRankAdd, a.T)) return expand_v<T, 1>(a, l, s);
@@ -1365,12 +1598,13 @@ hipError_t backward_t(const LowRankArgs& a, const LowRankLayout& l, hipStream_t 
 
 template <typename T>
 hipError_t project_t(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
+  if (few(kLowRankProject, a.T, a.S, a.n, a.R)) return few_t<T, true>(a, s);
   hipError_t e = shrink<T, false, true>(a, l, s);
   if (e != hipSuccess) return e;
   switch (l.width) {
-    case 1: return project_v<T, 1, 1>(a, l, s);
-    case 2: return project_v<T, 2, 1>(a, l, s);
-    default: return project_v<T, 4, 1>(a, l, s);
+    case 1: return project_v<T, 1>(a, l, s);
+    case 2: return project_v<T, 2>(a, l, s);
+    default: return project_v<T, 4>(a, l, s);
   }
 }
 
@@ -1379,6 +1613,7 @@ hipError_t project_t(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s
 LowRankLayout lowrank_layout(int op, int dtype, int64_t T, int64_t S, int64_t n, int64_t R,
                              int64_t n_in, int64_t n_out) {
   LowRankLayout l{};
+  if (few(op, T, S, n, R)) return l;  // one launch, nothing between
   const int64_t eb = dtype == kF32 ? 4 : 2;
   l.Tp = cdiv(T, 128) * 128;  // whole tiles
   l.width = token_width(op, dtype, T, R);

@@ -179,7 +179,7 @@ struct LowRank {
   }
   at::Tensor workspace(spops_low_rank_op op, size_t& bytes) const {
     status("spops_low_rank_workspace_size", spops_low_rank_workspace_size(&d, op, &bytes));
-    return at::empty({(int64_t)bytes}, xt.options().dtype(at::kByte));
+    return bytes ? at::empty({(int64_t)bytes}, xt.options().dtype(at::kByte)) : at::Tensor();
   }
 };
 
@@ -213,7 +213,7 @@ PyObject* low_rank_forward(PyObject* const* args, Py_ssize_t n, bool project) {
     const auto call = project ? spops_low_rank_project : spops_low_rank_add;
     status(project ? "spops_low_rank_project" : "spops_low_rank_add",
            call(&L.d, L.first.data_ptr(), L.ldf, L.xt.data_ptr(), L.ldx, out.data_ptr(),
-                leading(out, "out"), ws.data_ptr(), bytes, stream_of(L.xt.device())));
+                leading(out, "out"), ws.defined() ? ws.data_ptr() : nullptr, bytes, stream_of(L.xt.device())));
     if (into) {
       written(out);
       Py_INCREF(args[8]);
@@ -246,7 +246,7 @@ PyObject* low_rank_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     status("spops_low_rank_backward",
            spops_low_rank_backward(&L.d, L.first.data_ptr(), L.ldf, L.xt.data_ptr(), L.ldx,
                                    dx.data_ptr(), leading(dx, "dxt"), dA.data_ptr(), dB.data_ptr(),
-                                   ws.data_ptr(), bytes, stream_of(L.xt.device())));
+                                   ws.defined() ? ws.data_ptr() : nullptr, bytes, stream_of(L.xt.device())));
     return Py_BuildValue("(NNN)", THPVariable_Wrap(dx), THPVariable_Wrap(dA),
                          THPVariable_Wrap(dB));
   });
