@@ -1090,25 +1090,28 @@ __global__ __launch_bounds__(kThreads, 3) void lowrank_gradients_kernel(LowRankA
 
 // ---------------------------------------------------------------- project --
 
-// y = W x + B u on a tile of 16 V tokens: a workgroup takes 16 rows of W, eight
-// waves a slice of the features each; x comes as the fragments that the shrink
-// kernel packed.  V more waves make the adapters' part of 16 tokens each
+// y = W x + B u on a tile of 16 V tokens: a workgroup takes 16 MO rows of W,
+// eight waves a slice of the features each; x comes as the fragments that the
+// shrink kernel packed, and is read once for the MO row tiles.  V more waves make the adapters' part of 16 tokens each
 // meanwhile: their chain of dependent loads (u, adapter, B) is as long as the
 // stream of W and would double the time behind it.  All meet in shared memory.
-template <typename T, int V, bool SMALL>
+template <typename T, int V, int MO, bool SMALL>
 __global__ __launch_bounds__((kProjectWaves + V) * kWave) void lowrank_project_kernel(
     LowRankArgs a, int slices, int row_blocks) {
   constexpr int TT = 16 * V, D = 4;
   extern __shared__ float us[];
-  __shared__ f32x4 red[(kProjectWaves + 1) * V * kWave];
+  __shared__ f32x4 red[(kProjectWaves + 1) * MO * V * kWave];
   const int lane = lane_id(), n = lane % 16, g = lane / 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int block = blockIdx.x % row_blocks;
   const int64_t tile = blockIdx.x / row_blocks;
   int64_t t0 = tile * TT;
   if (t0 > a.T - TT) t0 = a.T > TT ? a.T - TT : 0;
-  const int64_t lim = a.T - V, o0 = (int64_t)block * 16;
-  const int64_t o = o0 + n, oc = o < a.n_out ? o : a.n_out - 1;
+  const int64_t lim = a.T - V, o0 = (int64_t)block * (16 * MO);
+  auto row_of = [&](int k) {
+    const int64_t o = o0 + k * 16 + n;
+    return o < a.n_out ? o : a.n_out - 1;
+  };
   // token of row m of tile j
   auto token = [&](int m, int j) {
     const int64_t t = t0 + m * V;
@@ -1117,20 +1120,23 @@ __global__ __launch_bounds__((kProjectWaves + V) * kWave) void lowrank_project_k
   if (wave < kProjectWaves) {
     const int64_t steps = cdiv(a.n_in, 32);
     const int64_t s0 = steps * wave / kProjectWaves, s1 = steps * (wave + 1) / kProjectWaves;
-    const T* w = (const T*)a.W + oc * a.ldw + g * 8;
-    const T* xp = (const T*)a.packed + (tile * steps * V * kWave + lane) * 8;
-    f32x4 acc[V];
+    const T* w[MO];
 #pragma unroll
-    for (int j = 0; j < V; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < MO; ++k) w[k] = (const T*)a.W + row_of(k) * a.ldw + g * 8;
+    const T* xp = (const T*)a.packed + (tile * steps * V * kWave + lane) * 8;
+    f32x4 acc[MO * V];
+#pragma unroll
+    for (int k = 0; k < MO * V; ++k) acc[k] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int64_t whole = a.n_in / 32 < s1 ? a.n_in / 32 : s1;
     // U steps' loads are issued together
-    constexpr int U = 8 / V;
+    constexpr int U = MO == 1 ? 8 / V : V == 4 ? 2 : 4;
     auto run = [&](int64_t at, auto steps_together) {
       constexpr int N = decltype(steps_together)::value;
-      Frag<T> fw[N], fx[N][V];
+      Frag<T> fw[N][MO], fx[N][V];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        fw[i] = load8(w + (at + i) * 32);
+#pragma unroll
+        for (int k = 0; k < MO; ++k) fw[i][k] = load8(w[k] + (at + i) * 32);
 #pragma unroll
         for (int j = 0; j < V; ++j) fx[i][j] = load8(xp + ((at + i) * V + j) * kWave * 8);
       }
@@ -1138,7 +1144,9 @@ __global__ __launch_bounds__((kProjectWaves + V) * kWave) void lowrank_project_k
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] = mma(fx[i][j], fw[i], acc[j]);
+        for (int k = 0; k < MO; ++k)
+#pragma unroll
+          for (int j = 0; j < V; ++j) acc[k * V + j] = mma(fx[i][j], fw[i][k], acc[k * V + j]);
     };
     int64_t s = s0;
 #pragma unroll 1
@@ -1146,12 +1154,17 @@ __global__ __launch_bounds__((kProjectWaves + V) * kWave) void lowrank_project_k
 #pragma unroll 1
     for (; s < whole; ++s) run(s, Int<1>{});
     if (s < s1) {
-      const Frag<T> fw = load8_count(w + s * 32, clampi(a.n_in - s * 32 - g * 8, 0, 8));
+      const int cnt = clampi(a.n_in - s * 32 - g * 8, 0, 8);
 #pragma unroll
-      for (int j = 0; j < V; ++j) acc[j] = mma(load8(xp + (s * V + j) * kWave * 8), fw, acc[j]);
+      for (int k = 0; k < MO; ++k) {
+        const Frag<T> fw = load8_count(w[k] + s * 32, cnt);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          acc[k * V + j] = mma(load8(xp + (s * V + j) * kWave * 8), fw, acc[k * V + j]);
+      }
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) red[(wave * V + j) * kWave + lane] = acc[j];
+    for (int k = 0; k < MO * V; ++k) red[(wave * MO * V + k) * kWave + lane] = acc[k];
   } else {
     const int j = wave - kProjectWaves, rs = staged_width(a.R);
     float* mine = us + j * 16 * rs;
@@ -1179,11 +1192,13 @@ __global__ __launch_bounds__((kProjectWaves + V) * kWave) void lowrank_project_k
       ra[i] = __shfl(ad_n, g * 4 + i, kWave);
       up[i] = __is_same(T, _Float16) ? __shfl(p.up, g * 4 + i, kWave) : 1.f;
     }
-    f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 v[MO];
+#pragma unroll
+    for (int m = 0; m < MO; ++m) v[m] = f32x4{0.f, 0.f, 0.f, 0.f};
     uint64_t rest = __ballot(ad_n >= 0);
     while (rest) {
       // D distinct adapters, their factors requested together
-      int ads[D], count = 0;
+      int ads[D], ranks[D], count = 0;
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         ads[d] = d > 0 ? ads[d - 1] : 0;
@@ -1193,35 +1208,49 @@ __global__ __launch_bounds__((kProjectWaves + V) * kWave) void lowrank_project_k
           ++count;
         }
       }
-      f32x4 c[D];
 #pragma unroll
-      for (int d = 0; d < D; ++d) c[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int d = 0; d < D; ++d) ranks[d] = rank_of(a, ads[d]);
+      f32x4 c[MO][D];
+#pragma unroll
+      for (int m = 0; m < MO; ++m)
+#pragma unroll
+        for (int d = 0; d < D; ++d) c[m][d] = f32x4{0.f, 0.f, 0.f, 0.f};
       for (int k = 0; k < blocks; ++k) {
         const Frag<T> hi = u_frag<T, SMALL>(row, k, false, p.down);
         const Frag<T> lo = u_frag<T, SMALL>(row, k, true, p.down);
-        Frag<T> f[D];
+        Frag<T> f[MO][D];
 #pragma unroll
-        for (int d = 0; d < D; ++d) f[d] = b_frag<T, SMALL>(a, ads[d], oc, rank_of(a, ads[d]), k);
+        for (int d = 0; d < D; ++d)
 #pragma unroll
-        for (int d = 0; d < D; ++d) c[d] = token_mma<T, SMALL>(hi, lo, f[d], c[d]);
+          for (int m = 0; m < MO; ++m) f[m][d] = b_frag<T, SMALL>(a, ads[d], row_of(m), ranks[d], k);
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+#pragma unroll
+          for (int m = 0; m < MO; ++m) c[m][d] = token_mma<T, SMALL>(hi, lo, f[m][d], c[m][d]);
       }
 #pragma unroll
       for (int d = 0; d < D; ++d)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = d < count && ra[i] == ads[d] ? c[d][i] * up[i] : v[i];
+        for (int i = 0; i < 4; ++i) {
+          const bool mine_too = d < count && ra[i] == ads[d];
+#pragma unroll
+          for (int m = 0; m < MO; ++m) v[m][i] = mine_too ? c[m][d][i] * up[i] : v[m][i];
+        }
     }
-    red[(kProjectWaves * V + j) * kWave + lane] = v;
+#pragma unroll
+    for (int m = 0; m < MO; ++m) red[((kProjectWaves * MO + m) * V + j) * kWave + lane] = v[m];
   }
   __syncthreads();
-  if (wave < V) {
-    f32x4 v = red[wave * kWave + lane];
+  for (int k = wave; k < MO * V; k += kProjectWaves + V) {
+    f32x4 v = red[k * kWave + lane];
 #pragma unroll
-    for (int h = 1; h < kProjectWaves; ++h) v += red[(h * V + wave) * kWave + lane];
-    const f32x4 add = red[(kProjectWaves * V + wave) * kWave + lane];
+    for (int h = 1; h < kProjectWaves; ++h) v += red[(h * MO * V + k) * kWave + lane];
+    const f32x4 add = red[(kProjectWaves * MO * V + k) * kWave + lane];
+    const int64_t o = o0 + k / V * 16 + n;
     if (o < a.n_out) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t t = token(g * 4 + i, wave);
+        const int64_t t = token(g * 4 + i, k % V);
         if (t < a.T) store_bits((T*)a.out + o * a.ldo + t, out_bits(v[i] + add[i], (T*)nullptr));
       }
     }
@@ -1543,18 +1572,29 @@ hipError_t gradients(const LowRankArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int V>
-hipError_t project_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
-  const int64_t rb = cdiv(a.n_out, 16);
+// Row tiles of a workgroup: as many as leave one workgroup to a CU, so that no
+// second round runs half empty and x is read less often (32 tokens, 11008 x
+// 4096 f16: MO1US us with one, MO3US us with three).
+template <typename T, int V, int MO>
+hipError_t project_vm(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
+  const int64_t rb = cdiv(a.n_out, 16 * MO);
   const dim3 grid((unsigned)(rb * cdiv(a.T, 16 * V))), block((kProjectWaves + V) * kWave);
   const size_t lds = staged_bytes(16 * V, a.R);
   if (a.R <= 16)
-    hipLaunchKernelGGL((lowrank_project_kernel<T, V, true>), grid, block, lds, s, a, l.slices_u,
+    hipLaunchKernelGGL((lowrank_project_kernel<T, V, MO, true>), grid, block, lds, s, a, l.slices_u,
                        (int)rb);
   else
-    hipLaunchKernelGGL((lowrank_project_kernel<T, V, false>), grid, block, lds, s, a, l.slices_u,
-                       (int)rb);
+    hipLaunchKernelGGL((lowrank_project_kernel<T, V, MO, false>), grid, block, lds, s, a,
+                       l.slices_u, (int)rb);
   return hipGetLastError();
+}
+
+template <typename T, int V>
+hipError_t project_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
+  const int64_t tiles = cdiv(a.n_out, 16) * cdiv(a.T, 16 * V);
+  if (tiles <= 256) return project_vm<T, V, 1>(a, l, s);
+  if (tiles <= 512) return project_vm<T, V, 2>(a, l, s);
+  return project_vm<T, V, 3>(a, l, s);
 }
 
 // One launch for up to 16 tokens where their distinct adapters cannot have
