@@ -899,7 +899,6 @@ __global__ __launch_bounds__(kThreads, 3) void lowrank_expand_kernel(LowRankArgs
 
 // ------------------------------------------------------------------ outer --
 
-constexpr int kOuterFeatures = 2;   // 16-feature rows of tiles a workgroup takes
 constexpr int kListTokens = 32 * kThreads;
 
 template <int FF, int NR>
@@ -917,10 +916,10 @@ struct OuterShared {
 // loads in flight; other adapters' tokens are masked out of both operands.
 // The waves' sums are added in a fixed order.  f16: the block's product is
 // scaled back in fp32 by the exponent that pack chose for the rank.
-template <typename T, int NR>
+template <typename T, int NR, int FF>
 __device__ __forceinline__ void outer_tile(const LowRankArgs& a, bool is_x, int64_t f0, int ad,
-                                           int r0, OuterShared<kOuterFeatures, NR>& sh) {
-  constexpr int FF = kOuterFeatures, P = NR * sizeof(T) > 4 ? 1 : 2;
+                                           int r0, OuterShared<FF, NR>& sh) {
+  constexpr int P = NR * sizeof(T) > 4 || FF > 2 ? 1 : 2;
   constexpr bool F16 = __is_same(T, _Float16), HALVES = sizeof(T) == 2;
   const int tid = threadIdx.x, lane = lane_id(), n = lane % 16, g = lane / 16, wave = tid / kWave;
   const int64_t F = is_x ? a.n_in : a.n_out, ld = is_x ? a.ldx : a.ldy;
@@ -1062,11 +1061,11 @@ __device__ __forceinline__ void outer_tile(const LowRankArgs& a, bool is_x, int6
 
 // dA, dB and dx in one launch: they need the same packed ranks and nothing of
 // each other, and the reads of the first two go beside the writes of the last.
-template <typename T, int NR, int STEPS, bool SMALL>
+template <typename T, int NR, int STEPS, bool SMALL, int FF>
 __global__ __launch_bounds__(kThreads, 3) void lowrank_gradients_kernel(LowRankArgs a, int xblocks,
                                                                      int yblocks, int tiles,
                                                                      int rows_per_block) {
-  constexpr int V = 16 / sizeof(T), TT = 16 * V, FF = kOuterFeatures;
+  constexpr int V = 16 / sizeof(T), TT = 16 * V;
   extern __shared__ __attribute__((aligned(16))) char operand[];
   __shared__ union {
     OuterShared<FF, NR> outer;
@@ -1075,9 +1074,10 @@ __global__ __launch_bounds__(kThreads, 3) void lowrank_gradients_kernel(LowRankA
   const int rcs = (a.R + 63) / 64;
   const int64_t outer = (int64_t)(xblocks + yblocks) * a.n * rcs;
   if (blockIdx.x < outer) {
-    const int per = a.n * rcs, fb = blockIdx.x / per, rest = blockIdx.x % per;
+    const uint32_t b = xcd_chunk(blockIdx.x, (uint32_t)outer);
+    const int per = a.n * rcs, fb = b / per, rest = b % per;
     const bool is_x = fb < xblocks;
-    outer_tile<T, NR>(a, is_x, (int64_t)(is_x ? fb : fb - xblocks) * (16 * FF), rest / rcs,
+    outer_tile<T, NR, FF>(a, is_x, (int64_t)(is_x ? fb : fb - xblocks) * (16 * FF), rest / rcs,
                       rest % rcs * 64, sh.outer);
   } else {
     const int64_t b = xcd_chunk(blockIdx.x - outer, gridDim.x - outer), t0 = b % tiles * TT, row0 = b / tiles * rows_per_block;
@@ -1260,32 +1260,37 @@ __global__ __launch_bounds__((kProjectWaves + V) * kWave) void lowrank_project_k
 // -------------------------------------------------------------------- few --
 
 constexpr int kFewTokens = 16;
+constexpr int kFewThreads = 1024;
+constexpr int kFewWaves = kFewThreads / kWave;
 
-// A few tokens with one adapter or two in one launch: every workgroup makes
-// u = A x for itself (from its XCD's L2, 128 KB for 16 ranks of 4096 features)
-// and then its rows: 16 of W and B (PROJECT: the waves split the features of
-// both W and A), or 128 of B (added to y).  Two launches cost more than the
-// repeated reads as long as a workgroup's share of A is no longer than twice
-// its rows of W: the rule below.
+// A few tokens with one adapter at most, in one launch: every workgroup makes
+// u = A x for itself, from its XCD's L2 (128 KB for 16 ranks of 4096 features).
+// add: sixteen waves split A's features, then take 16 rows of B each.  project:
+// a workgroup takes 16 rows of W, whose features eight waves split; the other
+// eight find the adapter and make u and B u meanwhile.
 template <typename T, bool PROJECT, int NR>
-__global__ __launch_bounds__(kProjectThreads) void lowrank_few_kernel(LowRankArgs a) {
+__global__ __launch_bounds__(kFewThreads) void lowrank_few_kernel(LowRankArgs a) {
   constexpr bool SMALL = NR == 1;
-  constexpr int U = 4;
-  extern __shared__ float us[];
-  __shared__ f32x4 red[kProjectWaves * (NR > 1 ? NR : 1) * kWave];
-  __shared__ TokenTile<kFewTokens> tile;
+  constexpr int AW = PROJECT ? kFewWaves - kProjectWaves : kFewWaves;  // waves that split A
+  __shared__ float us[16 * (16 * NR + 4)];
+  __shared__ f32x4 red[(AW * NR + (PROJECT ? kProjectWaves : 0)) * kWave];
+  f32x4* redw = red + AW * NR * kWave;
   const int lane = lane_id(), n = lane % 16, g = lane / 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const bool stream = PROJECT && wave >= AW;  // a wave of W
   const int64_t K = a.n_in, steps = cdiv(K, 32);
-  const int64_t s0 = steps * wave / kProjectWaves, s1 = steps * (wave + 1) / kProjectWaves;
+  const int parts = stream ? kProjectWaves : AW, part = stream ? wave - AW : wave;
+  const int64_t s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
   const int64_t whole = K / 32 < s1 ? K / 32 : s1;
-  const int tok = n < a.T ? n : (int)a.T - 1, rs = staged_width(a.R);
-  const T* x = (const T*)a.x + tok;
+  constexpr int rs = 16 * NR + 4;
+  const T* x = (const T*)a.x + (n < a.T ? n : (int)a.T - 1);
   const bool neighbours = a.ldx == 1;  // one token: the features lie together
-  auto x_frag = [&](int64_t k0) {
+  auto x_frag = [&](int64_t k0, auto tail) {
     uint32_t b[8];
+    const T* p = x + k0 * a.ldx;
 #pragma unroll
-    for (int s = 0; s < 8; ++s) b[s] = raw_bits(x + (k0 + s) * a.ldx);
+    for (int s = 0; s < 8; ++s)
+      b[s] = !decltype(tail)::value || k0 + s < K ? raw_bits(p + s * a.ldx) : 0u;
     Frag<T> f;
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
@@ -1296,21 +1301,7 @@ __global__ __launch_bounds__(kProjectThreads) void lowrank_few_kernel(LowRankArg
     }
     return f;
   };
-  auto x_tail = [&](int64_t k0) {
-    uint32_t b[8];
-#pragma unroll
-    for (int s = 0; s < 8; ++s) b[s] = k0 + s < K ? raw_bits(x + (k0 + s) * a.ldx) : 0u;
-    Frag<T> f;
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      if (sizeof(T) == 4)
-        f.w[s] = b[s];
-      else if (s % 2 == 0)
-        f.w[s / 2] = b[s] | b[s + 1] << 16;
-    }
-    return f;
-  };
-  // rows of M matrices of row length K against x, over this wave's features
+  // rows of length K against x, over this wave's features
   auto dots = [&](auto count, const T* const* rows, f32x4* acc) {
     constexpr int M = decltype(count)::value;
     int64_t s = s0;
@@ -1325,7 +1316,7 @@ __global__ __launch_bounds__(kProjectThreads) void lowrank_few_kernel(LowRankArg
         if constexpr (decltype(near)::value)
           fx[i] = load8(x + k0);
         else
-          fx[i] = x_frag(k0);
+          fx[i] = x_frag(k0, Int<0>{});
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -1334,6 +1325,7 @@ __global__ __launch_bounds__(kProjectThreads) void lowrank_few_kernel(LowRankArg
         for (int m = 0; m < M; ++m) acc[m] = mma(f[i][m], fx[i], acc[m]);
       s += N;
     };
+    constexpr int U = sizeof(T) == 4 ? 4 : 8;
     if (neighbours) {
 #pragma unroll 1
       while (s + U <= whole) run(Int<U>{}, Int<1>{});
@@ -1345,95 +1337,103 @@ __global__ __launch_bounds__(kProjectThreads) void lowrank_few_kernel(LowRankArg
     while (s < whole) run(Int<1>{}, Int<0>{});
     if (s < s1) {
       const int64_t k0 = s * 32 + g * 8;
-      const Frag<T> fx = x_tail(k0);
+      const Frag<T> fx = x_frag(k0, Int<1>{});
 #pragma unroll
       for (int m = 0; m < M; ++m)
         acc[m] = mma(load8_count(rows[m] + k0, clampi(K - k0, 0, 8)), fx, acc[m]);
     }
   };
   const int64_t o0 = PROJECT ? (int64_t)blockIdx.x * 16
-                             : ((int64_t)blockIdx.x * kProjectWaves + wave) * 16;
+                             : ((int64_t)blockIdx.x * kFewWaves + wave) * 16;
   const int64_t oc = o0 + n < a.n_out ? o0 + n : a.n_out - 1;
-  f32x4 accw[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
-  if constexpr (PROJECT) {
-    const T* rows[1] = {(const T*)a.W + oc * a.ldw};
-    dots(Int<1>{}, rows, accw);
-  }
-  for (int i = threadIdx.x; i < 16 * rs; i += kProjectThreads) us[i] = 0.f;
-  token_adapters<kFewTokens, kProjectThreads>(a, 0, tile);
-  // requested before u is made: the rows of y and of the first adapter's B
-  const bool rows_here = PROJECT ? wave == 0 : o0 < a.n_out;
+  const bool finish = PROJECT ? wave == 0 : o0 < a.n_out;  // waves that write rows
   float v[4] = {0.f, 0.f, 0.f, 0.f};
-  if (!PROJECT && rows_here && n < a.T) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t r = o0 + g * 4 + i;
-      if (r < a.n_out) v[i] = to_f32(((const T*)a.y)[r * a.ldy + n]);
-    }
-  }
-  AdapterWalk<kFewTokens> walk(tile.tok);
-  int ad, lead = -1;
+  int ad = -1, rank = 0;
+  float sc = 1.f;
+  uint32_t mine = 0;  // tokens of the adapter
   Frag<T> fb{};
-  while (walk.next(ad)) {
-    if (lead < 0) {
-      lead = ad;
-      if (rows_here) fb = b_frag<T, SMALL>(a, ad, oc, rank_of(a, ad), 0);
-    }
-    f32x4 acc[NR];
-    const T* rows[NR];
-#pragma unroll
-    for (int q = 0; q < NR; ++q) {
-      const int r = q * 16 + n;
-      rows[q] = (const T*)a.A + ((int64_t)ad * a.R + (r < a.R ? r : a.R - 1)) * K;
-      acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    dots(Int<NR>{}, rows, acc);
-#pragma unroll
-    for (int q = 0; q < NR; ++q) red[(wave * NR + q) * kWave + lane] = acc[q];
-    __syncthreads();
-    if (wave < NR && n < a.T && tile.tok[n] == ad) {
-      f32x4 t = red[wave * kWave + lane];
-#pragma unroll
-      for (int h = 1; h < kProjectWaves; ++h) t += red[(h * NR + wave) * kWave + lane];
-      const float sc = a.scale ? a.scale[ad] : 1.f;
-      const int rank = rank_of(a, ad);
+  if (stream) {
+    f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
+    const T* rows[1] = {(const T*)a.W + oc * a.ldw};
+    dots(Int<1>{}, rows, acc);
+    redw[part * kWave + lane] = acc[0];
+  } else {
+    if (!PROJECT && finish && n < a.T) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = wave * 16 + g * 4 + i;
-        if (r < rank) us[n * rs + r] = t[i] * sc;
+        const int64_t r = o0 + g * 4 + i;
+        if (r < a.n_out) v[i] = to_f32(((const T*)a.y)[r * a.ldy + n]);
       }
     }
-    __syncthreads();
-  }
-  if constexpr (PROJECT) {
-    red[wave * kWave + lane] = accw[0];
-    __syncthreads();
-    if (wave == 0) {
+    for (int i0 = 0; i0 < a.S; i0 += kWave) {
+      const int i = i0 + lane;
+      uint32_t m = 0;
+      int of = -1;
+      if (i < a.S) {
+        of = a.adapter[i];
+        const int lo = clampi(a.offsets[i], 0, (int)a.T), hi = clampi(a.offsets[i + 1], 0, (int)a.T);
+        if (lo < hi && of >= 0 && of < a.n) m = (1u << hi) - (1u << lo);
+      }
+      const uint64_t some = __ballot(m != 0);
+      if (some) {
+        if (ad < 0) ad = __builtin_amdgcn_readlane(of, __builtin_ctzll(some));
+        if (of != ad) m = 0;
 #pragma unroll
-      for (int h = 1; h < kProjectWaves; ++h) accw[0] += red[h * kWave + lane];
+        for (int o = 1; o < kWave; o <<= 1) m |= (uint32_t)__shfl_xor((int)m, o, kWave);
+        mine |= m;
+      }
+    }
+    if (ad >= 0) {
+      if (a.scale) sc = a.scale[ad];
+      rank = rank_of(a, ad);
+      if (rank == 0) mine = 0;
+      if (finish) fb = b_frag<T, SMALL>(a, ad, oc, rank, 0);
+      f32x4 acc[NR];
+      const T* rows[NR];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = accw[0][i];
+      for (int q = 0; q < NR; ++q) {
+        const int r = q * 16 + n;
+        rows[q] = (const T*)a.A + ((int64_t)ad * a.R + (r < a.R ? r : a.R - 1)) * K;
+        acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      dots(Int<NR>{}, rows, acc);
+#pragma unroll
+      for (int q = 0; q < NR; ++q) red[(wave * NR + q) * kWave + lane] = acc[q];
     }
   }
-  if (!rows_here) return;
+  __syncthreads();
+  if (wave < NR) {
+    f32x4 t = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (ad >= 0) {
+#pragma unroll
+      for (int h = 0; h < AW; ++h) t += red[(h * NR + wave) * kWave + lane];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = wave * 16 + g * 4 + i;
+      us[n * rs + r] = r < rank && ((mine >> n) & 1u) ? t[i] * sc : 0.f;
+    }
+  }
+  __syncthreads();
+  if (!finish) return;
+  if constexpr (PROJECT) {
+    f32x4 w = redw[lane];
+#pragma unroll
+    for (int h = 1; h < kProjectWaves; ++h) w += redw[h * kWave + lane];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = w[i];
+  }
   const float* row = us + n * rs;
   const Pow2 p = row_pow2<T>(row, a.R);
   const Frag<T> hi = u_frag<T, SMALL>(row, 0, false, p.down);
   const Frag<T> lo = u_frag<T, SMALL>(row, 0, true, p.down);
-  AdapterWalk<kFewTokens> again(tile.tok);
-  while (again.next(ad)) {
-    if (ad != lead) fb = b_frag<T, SMALL>(a, ad, oc, rank_of(a, ad), 0);
-    const f32x4 c = u_mma<T, SMALL>(fb, hi, lo, f32x4{0.f, 0.f, 0.f, 0.f});
-    if (tile.tok[n] == ad) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += c[i] * p.up;
-    }
-  }
+  const f32x4 c = u_mma<T, SMALL>(fb, hi, lo, f32x4{0.f, 0.f, 0.f, 0.f});
   if (n < a.T) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t r = o0 + g * 4 + i;
-      if (r < a.n_out) store_bits((T*)a.out + r * a.ldo + n, out_bits(v[i], (T*)nullptr));
+      const float f = (mine >> n) & 1u ? v[i] + c[i] * p.up : v[i];
+      if (r < a.n_out) store_bits((T*)a.out + r * a.ldo + n, out_bits(f, (T*)nullptr));
     }
   }
 }
@@ -1549,32 +1549,38 @@ hipError_t expand_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s)
   return hipGetLastError();
 }
 
-template <typename T>
-hipError_t gradients(const LowRankArgs& a, hipStream_t s) {
+template <typename T, int FF>
+hipError_t gradients_f(const LowRankArgs& a, hipStream_t s) {
   constexpr int TT = 256 / sizeof(T);
-  const int64_t xb = cdiv(a.n_in, 16 * kOuterFeatures), yb = cdiv(a.n_out, 16 * kOuterFeatures);
+  const int64_t xb = cdiv(a.n_in, 16 * FF), yb = cdiv(a.n_out, 16 * FF);
   const int64_t tiles = cdiv(a.T, TT), per = rows_per_block(a.n_in, tiles > 0 ? tiles : 1);
   const dim3 grid((unsigned)((xb + yb) * a.n * cdiv(a.R, 64) + cdiv(a.n_in, per) * tiles));
   const size_t lds = operand_bytes<16 / sizeof(T)>(a.R);
   const int t = (int)(tiles > 0 ? tiles : 1);
-  if (a.R <= 16)
-    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 1, 1, true>), grid, dim3(kThreads), lds, s, a,
-                       (int)xb, (int)yb, t, (int)per);
-  else if (a.R <= 32)
-    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 2, 1, false>), grid, dim3(kThreads), lds, s, a,
-                       (int)xb, (int)yb, t, (int)per);
-  else if (a.R <= 64)
-    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 4, 2, false>), grid, dim3(kThreads), lds, s, a,
-                       (int)xb, (int)yb, t, (int)per);
-  else
-    hipLaunchKernelGGL((lowrank_gradients_kernel<T, 4, 0, false>), grid, dim3(kThreads), lds, s, a,
-                       (int)xb, (int)yb, t, (int)per);
-  return hipGetLastError();
+  auto launch = [&](auto nr, auto steps, auto small) {
+    hipLaunchKernelGGL((lowrank_gradients_kernel<T, decltype(nr)::value, decltype(steps)::value,
+                                                 decltype(small)::value != 0, FF>),
+                       grid, dim3(kThreads), lds, s, a, (int)xb, (int)yb, t, (int)per);
+    return hipGetLastError();
+  };
+  if (a.R <= 16) return launch(Int<1>{}, Int<1>{}, Int<1>{});
+  if (a.R <= 32) return launch(Int<2>{}, Int<1>{}, Int<0>{});
+  if (a.R <= 64) return launch(Int<4>{}, Int<2>{}, Int<0>{});
+  return launch(Int<4>{}, Int<0>{}, Int<0>{});
+}
+
+// Features of an outer workgroup: 64 share each load of u where that still
+// gives two workgroups a CU (2047 tokens, 6 adapters of 32 ranks, f16: FF4US us
+// against FF2US with 32), else 32 (one adapter of 4096 x 4096).
+template <typename T>
+hipError_t gradients(const LowRankArgs& a, hipStream_t s) {
+  const int64_t wide = cdiv(a.n_in + a.n_out, 64) * a.n * cdiv(a.R, 64);
+  return wide >= kFillBlocks ? gradients_f<T, 4>(a, s) : gradients_f<T, 2>(a, s);
 }
 
 // Row tiles of a workgroup: as many as leave one workgroup to a CU, so that no
 // second round runs half empty and x is read less often (32 tokens, 11008 x
-// 4096 f16: MO1US us with one, MO3US us with three).
+// 4096 f16: 44 us with one, 29 with three).
 template <typename T, int V, int MO>
 hipError_t project_vm(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
   const int64_t rb = cdiv(a.n_out, 16 * MO);
@@ -1597,22 +1603,20 @@ hipError_t project_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s
   return project_vm<T, V, 3>(a, l, s);
 }
 
-// One launch for up to 16 tokens where their distinct adapters cannot have
-// more than 32 ranks together.
+// One launch for up to 16 tokens that cannot have more than one adapter, of up
+// to 32 ranks: two launches cost more than the repeated reads of A as long as a
+// workgroup reads no more of A than twice its rows of W.
 bool few(int op, int64_t T, int64_t S, int64_t n, int64_t R) {
-  int64_t distinct = S < T ? S : T;
-  distinct = distinct < n ? distinct : n;
-  return op != kLowRankBackward && T <= kFewTokens && R <= 32 && distinct * R <= 32;
+  return op != kLowRankBackward && T <= kFewTokens && R <= 32 && (T <= 1 || S <= 1 || n <= 1);
 }
 
 template <typename T, bool PROJECT>
 hipError_t few_t(const LowRankArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)cdiv(a.n_out, PROJECT ? 16 : 16 * kProjectWaves));
-  const size_t lds = staged_bytes(16, a.R);
+  const dim3 grid((unsigned)cdiv(a.n_out, PROJECT ? 16 : 16 * kFewWaves)), block(kFewThreads);
   if (a.R <= 16)
-    hipLaunchKernelGGL((lowrank_few_kernel<T, PROJECT, 1>), grid, dim3(kProjectThreads), lds, s, a);
+    hipLaunchKernelGGL((lowrank_few_kernel<T, PROJECT, 1>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((lowrank_few_kernel<T, PROJECT, 2>), grid, dim3(kProjectThreads), lds, s, a);
+    hipLaunchKernelGGL((lowrank_few_kernel<T, PROJECT, 2>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
