@@ -942,8 +942,26 @@ __device__ __forceinline__ void outer_tile(const LowRankArgs& a, bool is_x, int6
   f32x4 acc[FF * NR];
 #pragma unroll
   for (int k = 0; k < FF * NR; ++k) acc[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // 16-bit rows that start between two words are read as the words around them
+  // and shifted in registers: loads that are not aligned to a word take several
+  // times as long in this pattern (2047 tokens: 71 us where this takes 46)
+  const bool odd = HALVES && ((((uintptr_t)src) | (uintptr_t)(ld * (int64_t)sizeof(T))) & 2);
+  uint32_t shift[FF];
+#pragma unroll
+  for (int k = 0; k < FF; ++k) shift[k] = HALVES ? (uint32_t)((uintptr_t)row[k] & 2) * 8 : 0u;
+  struct Raw {
+    uint32_t w[2 * sizeof(T) + (HALVES ? 1 : 0)];
+  };
+  auto aligned = [&](const Raw& r, uint32_t sh) {
+    Frag<T> f;
+#pragma unroll
+    for (int i = 0; i < (int)(2 * sizeof(T)); ++i)
+      f.w[i] = HALVES ? __builtin_amdgcn_alignbit(r.w[HALVES ? i + 1 : i], r.w[i], sh) : r.w[i];
+    return f;
+  };
   struct Buf {
-    Frag<T> x[P][FF], hi[P][NR], lo[P][HALVES ? NR : 1];
+    Raw x[P][FF];
+    Frag<T> hi[P][NR], lo[P][HALVES ? NR : 1];
     uint32_t e[P][F16 ? NR : 1], m[P];
   } cur, nxt;
   for (int64_t c0 = 0; c0 < a.T; c0 += kListTokens) {
@@ -978,9 +996,33 @@ __device__ __forceinline__ void outer_tile(const LowRankArgs& a, bool is_x, int6
         b.m[p] = e + p < count ? __builtin_amdgcn_readfirstlane(sh.mask[blk]) : 0u;
         const int64_t bt = c0 + (int64_t)blk * 32, t = bt + g * 8;
         const bool whole = bt + 32 <= a.T;
+        if (!whole) {
 #pragma unroll
-        for (int k = 0; k < FF; ++k)
-          b.x[p][k] = whole ? load8(row[k] + t) : load8_count(row[k] + t, clampi(a.T - t, 0, 8));
+          for (int k = 0; k < FF; ++k) {
+            const Frag<T> f = load8_count(row[k] + t, clampi(a.T - t, 0, 8));
+            uint32_t below = 0;
+#pragma unroll
+            for (int i = 0; i < (int)(2 * sizeof(T)); ++i) {
+              b.x[p][k].w[i] = shift[k] ? __builtin_amdgcn_alignbit(f.w[i], below, 16) : f.w[i];
+              below = f.w[i];
+            }
+            if constexpr (HALVES) b.x[p][k].w[4] = below >> 16;
+          }
+        } else if (odd) {
+          // each word holds an element of the row: none lies outside its memory
+#pragma unroll
+          for (int k = 0; k < FF; ++k) {
+            const uint32_t* q = (const uint32_t*)((uintptr_t)(row[k] + t) & ~(uintptr_t)3);
+            __builtin_memcpy(b.x[p][k].w, q, 16);
+            if constexpr (HALVES) b.x[p][k].w[4] = q[shift[k] ? 4 : 3];
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < FF; ++k) {
+            __builtin_memcpy(b.x[p][k].w, row[k] + t, sizeof(Frag<T>));
+            if constexpr (HALVES) b.x[p][k].w[4] = 0u;
+          }
+        }
 #pragma unroll
         for (int q = 0; q < NR; ++q) {
           __builtin_memcpy(&b.hi[p][q], __builtin_assume_aligned(u + urow[q] + t, 16),
@@ -997,10 +1039,13 @@ __device__ __forceinline__ void outer_tile(const LowRankArgs& a, bool is_x, int6
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         if (b.m[p] == 0) continue;
+        Frag<T> x[FF];
+#pragma unroll
+        for (int k = 0; k < FF; ++k) x[k] = aligned(b.x[p][k], shift[k]);
         if (b.m[p] != ~0u) {
           const uint32_t m8 = (b.m[p] >> (g * 8)) & 255u;
 #pragma unroll
-          for (int k = 0; k < FF; ++k) mask8(b.x[p][k], m8);
+          for (int k = 0; k < FF; ++k) mask8(x[k], m8);
 #pragma unroll
           for (int q = 0; q < NR; ++q) {
             mask8(b.hi[p][q], m8);
@@ -1014,13 +1059,13 @@ __device__ __forceinline__ void outer_tile(const LowRankArgs& a, bool is_x, int6
             f32x4& d = acc[k * NR + q];
             if constexpr (F16) {
               const float up = __uint_as_float(b.e[p][q] << 23);
-              const f32x4 c = mma(b.x[p][k], b.lo[p][q],
-                                  mma(b.x[p][k], b.hi[p][q], f32x4{0.f, 0.f, 0.f, 0.f}));
+              const f32x4 c = mma(x[k], b.lo[p][q],
+                                  mma(x[k], b.hi[p][q], f32x4{0.f, 0.f, 0.f, 0.f}));
 #pragma unroll
               for (int i = 0; i < 4; ++i) d[i] = __builtin_fmaf(c[i], up, d[i]);
             } else {
-              d = mma(b.x[p][k], b.hi[p][q], d);
-              if constexpr (HALVES) d = mma(b.x[p][k], b.lo[p][q], d);
+              d = mma(x[k], b.hi[p][q], d);
+              if constexpr (HALVES) d = mma(x[k], b.lo[p][q], d);
             }
           }
       }
@@ -1570,8 +1615,8 @@ hipError_t gradients_f(const LowRankArgs& a, hipStream_t s) {
 }
 
 // Features of an outer workgroup: 64 share each load of u where that still
-// gives two workgroups a CU (2047 tokens, 6 adapters of 32 ranks, f16: FF4US us
-// against FF2US with 32), else 32 (one adapter of 4096 x 4096).
+// gives two workgroups a CU (2048 tokens, 6 adapters of 32 ranks, f16: 42 us
+// against 75 with 32), else 32 (one adapter of 4096 x 4096).
 template <typename T>
 hipError_t gradients(const LowRankArgs& a, hipStream_t s) {
   const int64_t wide = cdiv(a.n_in + a.n_out, 64) * a.n * cdiv(a.R, 64);
