@@ -3,11 +3,12 @@
 //   norm = sqrt(sum over all tensors of g^2),  c = min(1, max_norm / (norm + 1e-6)),
 //   out = c g   (in place, or into other tensors; a NaN norm gives NaN)
 //
-// Two launches for up to 128 tensors (and two more for each further 128): the
+// Two launches for up to 250 tensors (and two more for each further 250): the
 // squares' sums, one per workgroup; then every workgroup adds those sums in
-// the same order and scales its part.  The tensors' table travels in the
-// kernel arguments, so a call copies nothing to the device and may be
-// captured.  Sums are fp64: no square overflows, and the norm is exact to its
+// the same order and scales its part, its first values already requested.  The
+// tensors' table travels in the kernel arguments, 16 bytes a tensor with the
+// first launch (which leaves it in the workspace for the second) and 8 with the
+// second, so a call copies nothing to the device and may be captured.  Sums are fp64: no square overflows, and the norm is exact to its
 // fp32 rounding.  Bound by memory: the gradients are read twice and written
 // once.  The second pass runs through them backwards, so that what the first
 // read last is still in the 256 MB memory-side cache.
@@ -20,36 +21,50 @@ namespace spops {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTable = 128;      // tensors in one launch's arguments (under 4 KiB)
+// Tensors of one launch: its arguments stay under 4 KiB, and a full table of
+// the largest tensors has fewer chunks than an int counts.
+constexpr int kTable = 250;
 constexpr int64_t kChunk = 8192; // elements of a workgroup's step
-constexpr int64_t kMaxBlocks = 1024;  // four workgroups on each of the 256 CUs
+// Workgroups: six on each of the 256 CUs, for the tensors of a model's adapters
+// in one round (200 tensors, 12 million values: 28 us, 38 with four); four for
+// long streams (270 million f32 values: 599 us, 617 with six).
+constexpr int64_t kMaxBlocks = 1536;
+constexpr int64_t kStreamBlocks = 1024, kStreamChunks = 4 * kMaxBlocks;
 
 struct Table {
   const void* grad[kTable];
-  void* out[kTable];
-  int64_t numel[kTable];
-  uint8_t dtype[kTable];
   int32_t first[kTable + 1];  // first chunk of each tensor
+  // Elements of its last chunk less one, dtype above bit 13.  A word, not 16 bits:
+  // with both widths under one index the compiler (ROCm 7.2) forms the address of
+  // `first` from two halves of it, of which scalar loads drop the odd bits.
+  int32_t tail[kTable];
   int32_t count;
 };
+struct Outs {
+  void* out[kTable];
+};
+static_assert(kTable * (kClipMaxNumel / kChunk) + kMaxBlocks < INT32_MAX, "chunks");
+static_assert(sizeof(Table) + 16 <= 4096 && sizeof(Outs) + 64 <= 4096, "kernel arguments");
 
 struct Piece {
-  int tensor;
+  int tensor, dtype, n;
   int64_t at;  // first element
-  int n;
 };
 
-// The tensor of chunk c: each lane compares two of the table's starts.
+// The tensor of chunk c: lanes compare the table's starts.
 __device__ __forceinline__ Piece find_piece(const Table& t, int c) {
-  const int l = lane_id();
-  const uint64_t lo = __ballot(l < t.count && t.first[l] <= c);
-  const uint64_t hi = __ballot(l + kWave < t.count && t.first[l + kWave] <= c);
-  // empty tensors share their start with the next: the last start wins
+  int before = 0;
+#pragma unroll
+  for (int h = 0; h < (kTable + kWave - 1) / kWave; ++h) {
+    const int i = h * kWave + lane_id();
+    before += __builtin_popcountll(__ballot(i < t.count && t.first[i < kTable ? i : 0] <= c));
+  }
   Piece p;
-  p.tensor = __builtin_popcountll(lo) + __builtin_popcountll(hi) - 1;
+  p.tensor = before - 1;
+  const int tail = t.tail[p.tensor];
   p.at = (int64_t)(c - t.first[p.tensor]) * kChunk;
-  const int64_t left = t.numel[p.tensor] - p.at;
-  p.n = left < kChunk ? (int)left : (int)kChunk;
+  p.dtype = tail >> 13;
+  p.n = c + 1 == t.first[p.tensor + 1] ? (tail & 8191) + 1 : (int)kChunk;
   return p;
 }
 
@@ -90,87 +105,122 @@ __device__ __forceinline__ double squares(const T* g, int n) {
   return s;
 }
 
+// A whole chunk, 16 bytes a thread and load.
+struct Held {
+  Row<float, 4> w[kChunk * 4 / 16 / kThreads];
+};
+template <typename T>
+__device__ __forceinline__ void hold(const T* g, Held& h) {
+#pragma unroll
+  for (int k = 0; k < (int)(kChunk * sizeof(T) / 16 / kThreads); ++k)
+    __builtin_memcpy(&h.w[k], g + (k * kThreads + threadIdx.x) * (16 / sizeof(T)), 16);
+}
+template <typename T>
+__device__ __forceinline__ void scale_held(const Held& h, T* out, float c) {
+  constexpr int C = 16 / sizeof(T);
+#pragma unroll
+  for (int k = 0; k < (int)(kChunk / C / kThreads); ++k) {
+    const Row<T, C> r = __builtin_bit_cast(Row<T, C>, h.w[k]);
+    float v[C];
+#pragma unroll
+    for (int e = 0; e < C; ++e) v[e] = row_f32<T, C>(r, e) * c;
+    store_chunk<T, C>(out + (k * kThreads + threadIdx.x) * C, C, v);
+  }
+}
 template <typename T>
 __device__ __forceinline__ void scaled(const T* g, T* out, int n, float c) {
   constexpr int C = 16 / sizeof(T), STEP = kThreads * C;
-  if (n == kChunk) {
-    float v[kChunk / STEP][C];
+  for (int i = threadIdx.x * C; i < n; i += STEP) {
+    float v[C];
+    load_chunk<T, C>(g + i, n - i, v);
 #pragma unroll
-    for (int k = 0; k < kChunk / STEP; ++k)
-      load_chunk<T, C>(g + k * STEP + threadIdx.x * C, C, v[k]);
-#pragma unroll
-    for (int k = 0; k < kChunk / STEP; ++k) {
-#pragma unroll
-      for (int e = 0; e < C; ++e) v[k][e] *= c;
-      store_chunk<T, C>(out + k * STEP + threadIdx.x * C, C, v[k]);
-    }
-  } else {
-    for (int i = threadIdx.x * C; i < n; i += STEP) {
-      float v[C];
-      load_chunk<T, C>(g + i, n - i, v);
-#pragma unroll
-      for (int e = 0; e < C; ++e) v[e] *= c;
-      store_chunk<T, C>(out + i, n - i, v);
-    }
+    for (int e = 0; e < C; ++e) v[e] *= c;
+    store_chunk<T, C>(out + i, n - i, v);
   }
 }
 
-__global__ __launch_bounds__(kThreads) void clip_norm_kernel(const Table t, double* partial) {
+// f(typed null) for the storage type.
+template <typename F>
+__device__ __forceinline__ void with_type(int dtype, F f) {
+  if (dtype == kF32)
+    f((float*)nullptr);
+  else if (dtype == kF16)
+    f((_Float16*)nullptr);
+  else
+    f((bf16_t*)nullptr);
+}
+template <typename T>
+__device__ __forceinline__ T* typed(void* p, int64_t at, T*) {
+  return (T*)p + at;
+}
+template <typename T>
+__device__ __forceinline__ const T* typed(const void* p, int64_t at, T*) {
+  return (const T*)p + at;
+}
+
+__global__ __launch_bounds__(kThreads, 6) void clip_norm_kernel(const Table t, double* partial,
+                                                             Table* kept) {
   __shared__ double red[kThreads / kWave];
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < (int)(sizeof(Table) / 4); i += kThreads)
+      ((uint32_t*)kept)[i] = ((const uint32_t*)&t)[i];
   double s = 0.0;
   for (int c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
     const Piece p = find_piece(t, c);
-    const void* g = t.grad[p.tensor];
-    const int dt = t.dtype[p.tensor];
-    if (dt == kF32)
-      s += squares((const float*)g + p.at, p.n);
-    else if (dt == kF16)
-      s += squares((const _Float16*)g + p.at, p.n);
-    else
-      s += squares((const bf16_t*)g + p.at, p.n);
+    with_type(p.dtype, [&](auto* as) { s += squares(typed(t.grad[p.tensor], p.at, as), p.n); });
   }
   s = block_sum(s, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
-__global__ __launch_bounds__(kThreads) void clip_scale_kernel(const Table t, const double* partial,
-                                                              int partials, double max_norm,
-                                                              float* norm_out) {
+__global__ __launch_bounds__(kThreads) void clip_scale_kernel(const Outs outs, const Table* table,
+                                                              const double* partial, int partials,
+                                                              double max_norm, float* norm_out) {
   __shared__ double red[kThreads / kWave];
+  const Table& t = *table;
+  const int chunks = table ? t.first[t.count] : 0;
+  Held held;
+  Piece p{};
+  int b = blockIdx.x;
+  if (b < chunks) {
+    p = find_piece(t, chunks - 1 - b);
+    if (p.n == kChunk)
+      with_type(p.dtype, [&](auto* as) { hold(typed(t.grad[p.tensor], p.at, as), held); });
+  }
   double s = 0.0;
   for (int i = threadIdx.x; i < partials; i += kThreads) s += partial[i];
   const double norm = sqrt(block_sum(s, red));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
   const double q = max_norm / (norm + 1e-6);
   const float coef = q > 1.0 ? 1.f : (float)q;
-  const int chunks = t.first[t.count];
-  for (int b = blockIdx.x; b < chunks; b += gridDim.x) {
-    const Piece p = find_piece(t, chunks - 1 - b);
+  while (b < chunks) {
     const void* g = t.grad[p.tensor];
-    void* out = t.out[p.tensor];
-    if (out == g && coef == 1.f) continue;  // nothing changes
-    const int dt = t.dtype[p.tensor];
-    if (dt == kF32)
-      scaled((const float*)g + p.at, (float*)out + p.at, p.n, coef);
-    else if (dt == kF16)
-      scaled((const _Float16*)g + p.at, (_Float16*)out + p.at, p.n, coef);
-    else
-      scaled((const bf16_t*)g + p.at, (bf16_t*)out + p.at, p.n, coef);
+    void* out = outs.out[p.tensor];
+    if (out != g || coef != 1.f)  // or nothing changes
+      with_type(p.dtype, [&](auto* as) {
+        if (p.n == kChunk)
+          scale_held(held, typed(out, p.at, as), coef);
+        else
+          scaled(typed(g, p.at, as), typed(out, p.at, as), p.n, coef);
+      });
+    b += gridDim.x;
+    if (b >= chunks) break;
+    p = find_piece(t, chunks - 1 - b);
+    if (p.n == kChunk)
+      with_type(p.dtype, [&](auto* as) { hold(typed(t.grad[p.tensor], p.at, as), held); });
   }
 }
 
-// The table of tensors [i, count) as far as it goes; returns the next i.  The
-// caller keeps numel under kClipMaxNumel, so a full table has under 2^31 chunks.
-int64_t fill_table(const ClipTensor* ts, int64_t i, int64_t count, Table& t) {
+// The table of tensors [i, count) as far as it goes; returns the next i.
+int64_t fill_table(const ClipTensor* ts, int64_t i, int64_t count, Table& t, Outs& o) {
   t.count = 0;
   int64_t chunks = 0;
   for (; i < count && t.count < kTable; ++i) {
     const int64_t c = cdiv(ts[i].numel, kChunk);
     if (c == 0) continue;
+    o.out[t.count] = ts[i].out;
     t.grad[t.count] = ts[i].grad;
-    t.out[t.count] = ts[i].out;
-    t.numel[t.count] = ts[i].numel;
-    t.dtype[t.count] = (uint8_t)ts[i].dtype;
+    t.tail[t.count] = (int32_t)((ts[i].numel - 1) % kChunk) | ts[i].dtype << 13;
     t.first[t.count++] = (int32_t)chunks;
     chunks += c;
   }
@@ -180,39 +230,49 @@ int64_t fill_table(const ClipTensor* ts, int64_t i, int64_t count, Table& t) {
 
 int blocks_of(const Table& t) {
   const int64_t c = t.first[t.count];
-  return (int)(c < kMaxBlocks ? c : kMaxBlocks);
+  return (int)(c < kMaxBlocks ? c : c < kStreamChunks ? kMaxBlocks : kStreamBlocks);
 }
 
 }  // namespace
 
+// A table for each launch of a pass, then one fp64 sum per workgroup.
 size_t clip_workspace_bytes(int64_t count) {
-  return (size_t)((cdiv(count, kTable) + 1) * kMaxBlocks * 8);  // one fp64 sum per workgroup
+  return (size_t)(cdiv(count, kTable) + 1) * (sizeof(Table) + kMaxBlocks * 8);
 }
 
 hipError_t launch_clip(const ClipTensor* ts, int64_t count, double max_norm, float* norm, void* ws,
                        hipStream_t s) {
-  double* partial = (double*)ws;
+  Table* tables = (Table*)ws;
+  double* partial = (double*)(tables + cdiv(count, kTable) + 1);
   Table t;
-  int partials = 0;
+  Outs o;
+  int partials = 0, launches = 0;
   for (int64_t i = 0; i < count;) {
-    i = fill_table(ts, i, count, t);
+    i = fill_table(ts, i, count, t, o);
     const int blocks = blocks_of(t);
     if (blocks == 0) continue;
-    hipLaunchKernelGGL(clip_norm_kernel, dim3(blocks), dim3(kThreads), 0, s, t, partial + partials);
+    hipLaunchKernelGGL(clip_norm_kernel, dim3(blocks), dim3(kThreads), 0, s, t, partial + partials,
+                       tables + launches++);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     partials += blocks;
   }
-  bool first = true;
-  for (int64_t i = 0; i < count || first;) {
-    i = fill_table(ts, i, count, t);
+  if (launches == 0) {  // no values: the norm alone
+    hipLaunchKernelGGL(clip_scale_kernel, dim3(1), dim3(kThreads), 0, s, o, (const Table*)nullptr,
+                       partial, 0, max_norm, norm);
+    return hipGetLastError();
+  }
+  launches = 0;
+  for (int64_t i = 0; i < count;) {
+    i = fill_table(ts, i, count, t, o);
     const int blocks = blocks_of(t);
-    if (blocks == 0 && !(first && i >= count)) continue;
-    hipLaunchKernelGGL(clip_scale_kernel, dim3(blocks ? blocks : 1), dim3(kThreads), 0, s, t,
-                       partial, partials, max_norm, first ? norm : nullptr);
+    if (blocks == 0) continue;
+    hipLaunchKernelGGL(clip_scale_kernel, dim3(blocks), dim3(kThreads), 0, s, o,
+                       (const Table*)(tables + launches), partial, partials, max_norm,
+                       launches == 0 ? norm : nullptr);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    first = false;
+    ++launches;
   }
   return hipSuccess;
 }
