@@ -1485,6 +1485,12 @@ __global__ __launch_bounds__(kFewThreads) void lowrank_few_kernel(LowRankArgs a)
 
 // --------------------------------------------------------------- launches --
 
+constexpr size_t kSharedBytes = 160 * 1024;  // of a workgroup
+// The largest takers besides: expand and dx at 256 ranks (their tile's rows and
+// the adapters or the sums of outer), project with two row tiles.
+static_assert(128 * (1024 + 16) + sizeof(OuterShared<2, 4>) + 1024 <= kSharedBytes, "dx");
+static_assert((kProjectWaves + 1) * 2 * 4 * kWave * 16 + 64 * (256 + 4) * 4 <= kSharedBytes, "project");
+
 constexpr int64_t kFillBlocks = 512;  // two workgroups on each of the 256 CUs
 // Busy workgroups of the shrink kernel.  More of them mean more partial sums
 // (8192 tokens, 16 ranks: 25 us at 256, 27 at 384, 32 at 1024), fewer leave
@@ -1609,18 +1615,19 @@ hipError_t gradients_f(const LowRankArgs& a, hipStream_t s) {
     return hipGetLastError();
   };
   if (a.R <= 16) return launch(Int<1>{}, Int<1>{}, Int<1>{});
+  if constexpr (FF > 2) return launch(Int<2>{}, Int<1>{}, Int<0>{});
   if (a.R <= 32) return launch(Int<2>{}, Int<1>{}, Int<0>{});
   if (a.R <= 64) return launch(Int<4>{}, Int<2>{}, Int<0>{});
   return launch(Int<4>{}, Int<0>{}, Int<0>{});
 }
 
 // Features of an outer workgroup: 64 share each load of u where that still
-// gives two workgroups a CU (2048 tokens, 6 adapters of 32 ranks, f16: 42 us
+// gives two workgroups a CU and the sums fit the registers (2048 tokens, 6 adapters of 32 ranks, f16: 42 us
 // against 75 with 32), else 32 (one adapter of 4096 x 4096).
 template <typename T>
 hipError_t gradients(const LowRankArgs& a, hipStream_t s) {
-  const int64_t wide = cdiv(a.n_in + a.n_out, 64) * a.n * cdiv(a.R, 64);
-  return wide >= kFillBlocks ? gradients_f<T, 4>(a, s) : gradients_f<T, 2>(a, s);
+  const int64_t wide = cdiv(a.n_in + a.n_out, 64) * a.n;
+  return a.R <= 32 && wide >= kFillBlocks ? gradients_f<T, 4>(a, s) : gradients_f<T, 2>(a, s);
 }
 
 // Row tiles of a workgroup: as many as leave one workgroup to a CU, so that no
@@ -1644,7 +1651,9 @@ template <typename T, int V>
 hipError_t project_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
   const int64_t tiles = cdiv(a.n_out, 16) * cdiv(a.T, 16 * V);
   if (tiles <= 256) return project_vm<T, V, 1>(a, l, s);
-  if (tiles <= 512) return project_vm<T, V, 2>(a, l, s);
+  // three tiles' sums of 64 tokens leave no room for the ranks past 192
+  const size_t three = (kProjectWaves + 1) * 3 * V * kWave * sizeof(f32x4) + staged_bytes(16 * V, a.R);
+  if (tiles <= 512 || three > kSharedBytes) return project_vm<T, V, 2>(a, l, s);
   return project_vm<T, V, 3>(a, l, s);
 }
 
