@@ -518,6 +518,7 @@ __device__ __forceinline__ void stage_u(const LowRankArgs& a, const float* u, in
     float v = 0.f;
     if (r < a.R && t0 + t < a.T) {
       const float* p = u + (int64_t)r * a.Tp + t0 + t;
+#pragma unroll 8
       for (int s = 0; s < slices; ++s) v += p[(int64_t)s * a.R * a.Tp];
     }
     us[t * rs + r] = v;
@@ -784,7 +785,7 @@ template <typename T, int V, int STEPS, bool SMALL, bool DX>
 __device__ __forceinline__ void stream_rows(const LowRankArgs& a, const TileAdapters<16 * V>& tile,
                                             const char* staged, int64_t t0, int64_t row0,
                                             int64_t row_end) {
-  constexpr int D = V == 1 ? 4 : 1, N = STEPS > 0 ? STEPS : 1;
+  constexpr int D = V != 1 ? 1 : SMALL && sizeof(T) == 2 ? 8 : 4, N = STEPS > 0 ? STEPS : 1;
   const int lane = lane_id(), n = lane % 16, wave = threadIdx.x / kWave;
   const UOperand<T, V, SMALL> u(a, t0, staged);
   const int64_t rows = DX ? a.n_in : a.n_out, t = t0 + n * V;
@@ -814,12 +815,13 @@ __device__ __forceinline__ void stream_rows(const LowRankArgs& a, const TileAdap
       for (int k = 0; k < N; ++k) fn[d][k] = factor(d, ob, k);
   }
   for (; ob < row_end; ob += kWaves * 16) {
-    const int64_t next = ob + kWaves * 16 < row_end ? ob + kWaves * 16 : ob;
+    const int64_t next = ob + kWaves * 16;
+    const bool more = next < row_end;
     float v[4][V];
     if constexpr (!DX) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) yv[i] = yn[i];
-      load_rows<T, V>(y, a.ldy, next, rows, t, cnt, yn);
+      if (more) load_rows<T, V>(y, a.ldy, next, rows, t, cnt, yn);
     }
     if (STEPS > 0 && count > 0) {
 #pragma unroll
@@ -827,7 +829,7 @@ __device__ __forceinline__ void stream_rows(const LowRankArgs& a, const TileAdap
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           f[d][k] = fn[d][k];
-          fn[d][k] = factor(d, next, k);
+          if (more) fn[d][k] = factor(d, next, k);
         }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -880,8 +882,16 @@ __device__ __forceinline__ void stream_rows(const LowRankArgs& a, const TileAdap
 
 // Token tiles are the fastest index, so that neighbouring workgroups stream
 // neighbouring parts of the same rows.
+// Waves a SIMD that expand's registers are fitted to: three, two where three
+// would spill.
 template <typename T, int V, int STEPS, bool SMALL>
-__global__ __launch_bounds__(kThreads, 3) void lowrank_expand_kernel(LowRankArgs a, int slices,
+constexpr int expand_waves() {
+  return V == 1 ? (STEPS == 2 && sizeof(T) == 4 ? 2 : 3)
+                : (__is_same(T, _Float16) && (SMALL || STEPS == 2) ? 2 : 3);
+}
+
+template <typename T, int V, int STEPS, bool SMALL>
+__global__ __launch_bounds__(kThreads, (expand_waves<T, V, STEPS, SMALL>())) void lowrank_expand_kernel(LowRankArgs a, int slices,
                                                                   int tiles, int rows_per_block) {
   constexpr int TT = 16 * V;
   extern __shared__ __attribute__((aligned(16))) char operand[];
@@ -1220,7 +1230,7 @@ __global__ __launch_bounds__((kProjectWaves + V) * kWave) void lowrank_project_k
       float v = 0.f;
       if (r < a.R) {
         const float* p = a.u + (int64_t)r * a.Tp + tn;
-#pragma unroll 4
+#pragma unroll 8
         for (int s = 0; s < slices; ++s) v += p[(int64_t)s * a.R * a.Tp];
       }
       mine[n * rs + r] = v;
