@@ -1642,7 +1642,7 @@ hipError_t gradients(const LowRankArgs& a, hipStream_t s) {
 
 // Row tiles of a workgroup: as many as leave one workgroup to a CU, so that no
 // second round runs half empty and x is read less often (32 tokens, 11008 x
-// 4096 f16: 44 us with one, 29 with three).
+// 4096 f16: 44 us with one, 28 with three).
 template <typename T, int V, int MO>
 hipError_t project_vm(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
   const int64_t rb = cdiv(a.n_out, 16 * MO);
