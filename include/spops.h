@@ -471,7 +471,8 @@ typedef enum spops_low_rank_op {
 } spops_low_rank_op;
 
 /* Workspace bytes of a call (only the sizes and dtype of L are read).  The
- * workspace must be 256-byte aligned; its contents need no preparation. */
+ * workspace must be 256-byte aligned (NULL where the call needs none); its
+ * contents need no preparation. */
 spops_status spops_low_rank_workspace_size(const spops_low_rank* L, spops_low_rank_op op,
                                            size_t* bytes);
 /* out = yt + adapters(xt).  yt, out: [out_features][tokens] (out may be yt);

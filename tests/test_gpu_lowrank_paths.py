@@ -37,6 +37,12 @@ MANY = {
     "adapters-in-every-tile": dict(lengths=[(7 * i) % 23 for i in range(60)],
                                    adapter=[(11 * i) % 26 for i in range(60)], n=26, R=24,
                                    n_in=640, n_out=704),
+    "192-tokens": dict(lengths=[192], adapter=[0], n=1, R=40, n_in=96, n_out=130),
+    "193-tokens": dict(lengths=[193], adapter=[0], n=1, R=40, n_in=96, n_out=130),
+    "256-requests": dict(lengths=[1] * 256, adapter=[i % 7 - 1 for i in range(256)], n=6, R=16,
+                         n_in=160, n_out=100),
+    "257-requests": dict(lengths=[1] * 257, adapter=[i % 7 - 1 for i in range(257)], n=6, R=16,
+                         n_in=160, n_out=100),
     "64-ranks": dict(lengths=[(37 * i) % 90 + 1 for i in range(31)],
                      adapter=[(5 * i) % 8 - 1 for i in range(31)], n=7, R=64, n_in=321, n_out=384),
     "odd-rows": dict(lengths=[500, 1, 546], adapter=[0, 1, 0], n=2, R=32, n_in=200, n_out=216),

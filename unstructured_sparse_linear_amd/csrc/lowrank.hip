@@ -21,7 +21,7 @@
 //   pack     adds the slices and splits them into operands, where they are
 //            read many times
 //   expand   y + B u
-//   gradients  dA and dB, one workgroup per adapter and 32 features, and
+//   gradients  dA and dB, one workgroup per adapter and 32 or 64 features, and
 //            dx = A^T du
 //   project  W x + B u on the tokens of a decode step
 //   few      either forward on a few tokens in one launch
@@ -42,8 +42,7 @@ struct Int {
 
 constexpr int kThreads = 256;       // four waves
 constexpr int kWaves = kThreads / kWave;
-constexpr int kProjectThreads = 512;  // project: eight waves
-constexpr int kProjectWaves = kProjectThreads / kWave;
+constexpr int kProjectWaves = 8;    // that stream W
 
 // Workgroup b of N runs on XCD b % 8.  Each XCD takes one contiguous part of
 // the work list: neighbouring tiles share lines, factors and pages of one L2.
@@ -1576,11 +1575,16 @@ int64_t rows_per_block(int64_t rows, int64_t tiles) {
   return per < 512 ? per : 512;
 }
 
-// Tokens up to this many go through expand 16 to a tile, without the pack
-// launch.
-constexpr int64_t kStagedTokens = 128;
-
-bool packs(int op, int64_t T) { return op == kLowRankBackward || (op == kLowRankAdd && T > kStagedTokens); }
+// Whether the ranks are packed for expand's wide tiles, or staged by its
+// 16-token tiles without that launch: staged for few tokens, and for some more
+// where most tiles have many adapters (which a wide tile computes one after
+// another).  4096 x 4096, 16 ranks, bf16, staged against packed, us: one request
+// of 128 tokens 13.9 and 17.0, of 192 14.8 and 17.8, of 256 18.1 and 17.6; 256
+// requests of one token 33 and 42.
+bool packs(int op, int64_t T, int64_t S) {
+  if (op != kLowRankAdd) return op == kLowRankBackward;
+  return T > (S >= T / 8 ? 256 : 192);
+}
 
 template <typename T, bool BACKWARD>
 hipError_t pack(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
@@ -1668,8 +1672,9 @@ hipError_t project_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s
 }
 
 // One launch for up to 16 tokens that cannot have more than one adapter, of up
-// to 32 ranks: two launches cost more than the repeated reads of A as long as a
-// workgroup reads no more of A than twice its rows of W.
+// to 32 ranks (a workgroup of project then reads no more of A than twice its
+// rows of W).  One token of 4096 x 4096, 16 ranks, bf16: add 9.2 us where two
+// launches take 13.6, project 13.3 where they take 17.7.
 bool few(int op, int64_t T, int64_t S, int64_t n, int64_t R) {
   return op != kLowRankBackward && T <= kFewTokens && R <= 32 && (T <= 1 || S <= 1 || n <= 1);
 }
@@ -1689,7 +1694,7 @@ hipError_t add_t(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
   if (few(kLowRankAdd, a.T, a.S, a.n, a.R)) return few_t<T, false>(a, s);
   hipError_t e = shrink<T, false, false>(a, l, s);
   if (e != hipSuccess) return e;
-  if (!packs(kLowRankAdd, a.T)) return expand_v<T, 1>(a, l, s);
+  if (!packs(kLowRankAdd, a.T, a.S)) return expand_v<T, 1>(a, l, s);
   if ((e = pack<T, false>(a, l, s)) != hipSuccess) return e;
   return expand_v<T, 16 / sizeof(T)>(a, l, s);
 }
@@ -1745,7 +1750,7 @@ LowRankLayout lowrank_layout(int op, int dtype, int64_t T, int64_t S, int64_t n,
   l.at_packed = take(op == kLowRankProject
                          ? (size_t)(tiles * cdiv(n_in, 32) * l.width * kWave * 8 * eb)
                          : 0);
-  const bool rows = packs(op, T), sides = op == kLowRankBackward;
+  const bool rows = packs(op, T, S), sides = op == kLowRankBackward;
   l.at_rows = take(rows ? (size_t)l.Tp * packed_row((int)R) : 0);
   l.at_up = take(rows ? (size_t)l.Tp * 4 : 0);
   l.at_ru = take(sides ? (size_t)R * l.Tp * 4 : 0);
