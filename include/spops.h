@@ -467,7 +467,9 @@ typedef struct spops_low_rank {
 typedef enum spops_low_rank_op {
   SPOPS_LOW_RANK_ADD = 0,
   SPOPS_LOW_RANK_PROJECT = 1,
-  SPOPS_LOW_RANK_BACKWARD = 2
+  SPOPS_LOW_RANK_BACKWARD = 2,
+  /* added to ADD or PROJECT where out shares memory with xt */
+  SPOPS_LOW_RANK_OVER_X = 4
 } spops_low_rank_op;
 
 /* Workspace bytes of a call (only the sizes and dtype of L are read).  The
@@ -476,7 +478,10 @@ typedef enum spops_low_rank_op {
 spops_status spops_low_rank_workspace_size(const spops_low_rank* L, spops_low_rank_op op,
                                            size_t* bytes);
 /* out = yt + adapters(xt).  yt, out: [out_features][tokens] (out may be yt);
- * xt: [in_features][tokens]. */
+ * xt: [in_features][tokens].  Here and in project, out may share memory with xt
+ * (yt may be xt too): such a call needs the workspace of an op with
+ * SPOPS_LOW_RANK_OVER_X, since a call without one reads xt while it writes out.
+ * out overlaps no other input. */
 spops_status spops_low_rank_add(const spops_low_rank* L, const void* yt, int64_t ldy,
                                 const void* xt, int64_t ldx, void* out, int64_t ldo,
                                 void* workspace, size_t workspace_bytes, void* hip_stream);
@@ -491,7 +496,8 @@ spops_status spops_low_rank_project(const spops_low_rank* L, const void* W, int6
  *   dxt [in_features][tokens] = sum s A^T B^T dy (zero on tokens without an
  *       adapter; the projection's own W^T dy is not included),
  *   dA [adapters][rank][in_features], dB [adapters][out_features][rank], both
- *       written whole (zeros for unused adapters and past an adapter's rank). */
+ *       written whole (zeros for unused adapters and past an adapter's rank).
+ * The outputs overlap no input. */
 spops_status spops_low_rank_backward(const spops_low_rank* L, const void* dyt, int64_t ldy,
                                      const void* xt, int64_t ldx, void* dxt, int64_t lddx,
                                      void* dA, void* dB, void* workspace, size_t workspace_bytes,

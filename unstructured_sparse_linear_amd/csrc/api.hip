@@ -921,11 +921,22 @@ spops_status check_low_rank(const spops_low_rank* L) {
   return SPOPS_OK;
 }
 
+// Whether two matrices of `tokens` columns may share memory (their whole spans
+// meet; rows of one between rows of the other count too).
+bool spans_meet(const void* a, int64_t rows_a, int64_t lda, const void* b, int64_t rows_b,
+                int64_t ldb, int64_t tokens, int64_t bytes) {
+  const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
+  const auto end = [=](uintptr_t p, int64_t rows, int64_t ld) {
+    return p + ((uintptr_t)(rows - 1) * (uintptr_t)ld + (uintptr_t)tokens) * (uintptr_t)bytes;
+  };
+  return pa < end(pb, rows_b, ldb) && pb < end(pa, rows_a, lda);
+}
+
 // Sizes, leading dimensions, pointers and workspace of a call, and its launch
-// arguments.  `second` is y, dy or null; n_second its rows.
+// arguments.  `second` is y, dy or W.
 spops_status low_rank_args(const spops_low_rank* L, int op, const void* second, int64_t lds,
                            const void* xt, int64_t ldx, void* out, int64_t ldo, void* workspace,
-                           size_t bytes, LowRankArgs& a) {
+                           size_t bytes, LowRankArgs& a, bool& over_x) {
   const spops_status st = check_low_rank(L);
   if (st != SPOPS_OK) return st;
   if (ldx < L->tokens || ldo < L->tokens) return SPOPS_ERR_SHAPE;
@@ -942,8 +953,11 @@ spops_status low_rank_args(const spops_low_rank* L, int op, const void* second, 
   if (!L->A || !L->B || (L->requests > 0 && (!L->offsets || !L->adapter))) return SPOPS_ERR_NULL;
   if (L->tokens > 0) {
     if (!second || !xt || !out) return SPOPS_ERR_NULL;
-    const LowRankLayout l = lowrank_layout(op, L->dtype, L->tokens, L->requests, L->adapters,
-                                           L->rank, L->in_features, L->out_features);
+    over_x = op != kLowRankBackward &&
+             spans_meet(out, L->out_features, ldo, xt, L->in_features, ldx, L->tokens,
+                        L->dtype == SPOPS_F32 ? 4 : 2);
+    const LowRankLayout l = lowrank_layout(op, over_x, L->dtype, L->tokens, L->requests,
+                                           L->adapters, L->rank, L->in_features, L->out_features);
     if (l.bytes > 0 && (!workspace || bytes < l.bytes || ((uintptr_t)workspace & 255)))
       return SPOPS_ERR_WORKSPACE;
   }
@@ -980,11 +994,13 @@ spops_status spops_low_rank_workspace_size(const spops_low_rank* L, spops_low_ra
   const spops_status st = check_low_rank(L);
   if (st != SPOPS_OK) return st;
   if (!bytes) return SPOPS_ERR_NULL;
-  if (op != SPOPS_LOW_RANK_ADD && op != SPOPS_LOW_RANK_PROJECT && op != SPOPS_LOW_RANK_BACKWARD)
+  const bool over_x = ((int)op & SPOPS_LOW_RANK_OVER_X) != 0;
+  const int what = (int)op & ~SPOPS_LOW_RANK_OVER_X;
+  if (what != kLowRankAdd && what != kLowRankProject && (what != kLowRankBackward || over_x))
     return SPOPS_ERR_UNSUPPORTED;
   *bytes = L->tokens == 0 ? 0
-                          : lowrank_layout(op, L->dtype, L->tokens, L->requests, L->adapters,
-                                           L->rank, L->in_features, L->out_features)
+                          : lowrank_layout(what, over_x, L->dtype, L->tokens, L->requests,
+                                           L->adapters, L->rank, L->in_features, L->out_features)
                                 .bytes;
   return SPOPS_OK;
 }
@@ -993,20 +1009,24 @@ spops_status spops_low_rank_add(const spops_low_rank* L, const void* yt, int64_t
                                 const void* xt, int64_t ldx, void* out, int64_t ldo,
                                 void* workspace, size_t workspace_bytes, void* hip_stream) {
   LowRankArgs a{};
+  bool over_x = false;
   const spops_status st = low_rank_args(L, kLowRankAdd, yt, ldy, xt, ldx, out, ldo, workspace,
-                                        workspace_bytes, a);
+                                        workspace_bytes, a, over_x);
   if (st != SPOPS_OK || a.T == 0) return st;
-  return from_hip(launch_lowrank(kLowRankAdd, L->dtype, a, workspace, as_stream(hip_stream)));
+  return from_hip(launch_lowrank(kLowRankAdd, over_x, L->dtype, a, workspace,
+                                 as_stream(hip_stream)));
 }
 
 spops_status spops_low_rank_project(const spops_low_rank* L, const void* W, int64_t ldw,
                                     const void* xt, int64_t ldx, void* out, int64_t ldo,
                                     void* workspace, size_t workspace_bytes, void* hip_stream) {
   LowRankArgs a{};
+  bool over_x = false;
   const spops_status st = low_rank_args(L, kLowRankProject, W, ldw, xt, ldx, out, ldo, workspace,
-                                        workspace_bytes, a);
+                                        workspace_bytes, a, over_x);
   if (st != SPOPS_OK || a.T == 0) return st;
-  return from_hip(launch_lowrank(kLowRankProject, L->dtype, a, workspace, as_stream(hip_stream)));
+  return from_hip(launch_lowrank(kLowRankProject, over_x, L->dtype, a, workspace,
+                                 as_stream(hip_stream)));
 }
 
 spops_status spops_low_rank_backward(const spops_low_rank* L, const void* dyt, int64_t ldy,
@@ -1014,13 +1034,15 @@ spops_status spops_low_rank_backward(const spops_low_rank* L, const void* dyt, i
                                      void* dA, void* dB, void* workspace, size_t workspace_bytes,
                                      void* hip_stream) {
   LowRankArgs a{};
+  bool over_x = false;
   const spops_status st = low_rank_args(L, kLowRankBackward, dyt, ldy, xt, ldx, dxt, lddx,
-                                        workspace, workspace_bytes, a);
+                                        workspace, workspace_bytes, a, over_x);
   if (st != SPOPS_OK) return st;
   if (!dA || !dB) return SPOPS_ERR_NULL;
   a.dA = dA;
   a.dB = dB;
-  return from_hip(launch_lowrank(kLowRankBackward, L->dtype, a, workspace, as_stream(hip_stream)));
+  return from_hip(launch_lowrank(kLowRankBackward, over_x, L->dtype, a, workspace,
+                                 as_stream(hip_stream)));
 }
 
 // ------------------------------------------- gradient norm and clipping --

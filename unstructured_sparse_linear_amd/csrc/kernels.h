@@ -430,11 +430,13 @@ struct LowRankLayout {
   int width;               // tokens a lane holds of a row (tile: 16 width)
   int groups;              // workgroups that share a tile's adapters
   int slices_u, slices_du; // slices of the features
+  bool few;                // one launch, which reads x while it writes out
   size_t at_tokad, at_u, at_du, at_packed, at_rows, at_up, at_ru, at_rdu, at_eu, at_edu, bytes;
 };
-LowRankLayout lowrank_layout(int op, int dtype, int64_t T, int64_t S, int64_t n, int64_t R,
-                             int64_t n_in, int64_t n_out);
-hipError_t launch_lowrank(int op, int dtype, LowRankArgs a, void* ws, hipStream_t s);
+// over_x: out shares memory with x (only where op is not backward).
+LowRankLayout lowrank_layout(int op, bool over_x, int dtype, int64_t T, int64_t S, int64_t n,
+                             int64_t R, int64_t n_in, int64_t n_out);
+hipError_t launch_lowrank(int op, bool over_x, int dtype, LowRankArgs a, void* ws, hipStream_t s);
 
 // -------------------------------------------- gradient norm and clipping --
 struct ClipTensor {

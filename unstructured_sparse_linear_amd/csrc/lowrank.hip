@@ -1675,7 +1675,8 @@ hipError_t project_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s
 // One launch for up to 16 tokens that cannot have more than one adapter, of up
 // to 32 ranks (a workgroup of project then reads no more of A than twice its
 // rows of W).  One token of 4096 x 4096, 16 ranks, bf16: add 9.2 us where two
-// launches take 13.6, project 13.3 where they take 17.7.
+// launches take 13.6, project 13.3 where they take 17.7.  Its workgroups read x
+// while others write: not where out shares memory with x.
 bool few(int op, int64_t T, int64_t S, int64_t n, int64_t R) {
   return op != kLowRankBackward && T <= kFewTokens && R <= 32 && (T <= 1 || S <= 1 || n <= 1);
 }
@@ -1692,7 +1693,7 @@ hipError_t few_t(const LowRankArgs& a, hipStream_t s) {
 
 template <typename T>
 hipError_t add_t(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
-  if (few(kLowRankAdd, a.T, a.S, a.n, a.R)) return few_t<T, false>(a, s);
+  if (l.few) return few_t<T, false>(a, s);
   hipError_t e = shrink<T, false, false>(a, l, s);
   if (e != hipSuccess) return e;
   if (!packs(kLowRankAdd, a.T, a.S)) return expand_v<T, 1>(a, l, s);
@@ -1712,7 +1713,7 @@ hipError_t backward_t(const LowRankArgs& a, const LowRankLayout& l, hipStream_t 
 
 template <typename T>
 hipError_t project_t(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
-  if (few(kLowRankProject, a.T, a.S, a.n, a.R)) return few_t<T, true>(a, s);
+  if (l.few) return few_t<T, true>(a, s);
   hipError_t e = shrink<T, false, true>(a, l, s);
   if (e != hipSuccess) return e;
   switch (l.width) {
@@ -1724,10 +1725,11 @@ hipError_t project_t(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s
 
 }  // namespace
 
-LowRankLayout lowrank_layout(int op, int dtype, int64_t T, int64_t S, int64_t n, int64_t R,
-                             int64_t n_in, int64_t n_out) {
+LowRankLayout lowrank_layout(int op, bool over_x, int dtype, int64_t T, int64_t S, int64_t n,
+                             int64_t R, int64_t n_in, int64_t n_out) {
   LowRankLayout l{};
-  if (few(op, T, S, n, R)) return l;  // one launch, nothing between
+  l.few = !over_x && few(op, T, S, n, R);
+  if (l.few) return l;  // one launch, nothing between
   const int64_t eb = dtype == kF32 ? 4 : 2;
   l.Tp = cdiv(T, 128) * 128;  // whole tiles
   l.width = token_width(op, dtype, T, R);
@@ -1762,8 +1764,9 @@ LowRankLayout lowrank_layout(int op, int dtype, int64_t T, int64_t S, int64_t n,
   return l;
 }
 
-hipError_t launch_lowrank(int op, int dtype, LowRankArgs a, void* ws, hipStream_t s) {
-  const LowRankLayout l = lowrank_layout(op, dtype, a.T, a.S, a.n, a.R, a.n_in, a.n_out);
+hipError_t launch_lowrank(int op, bool over_x, int dtype, LowRankArgs a, void* ws,
+                          hipStream_t s) {
+  const LowRankLayout l = lowrank_layout(op, over_x, dtype, a.T, a.S, a.n, a.R, a.n_in, a.n_out);
   char* w = (char*)ws;
   a.Tp = l.Tp;
   a.tokad = (int32_t*)(w + l.at_tokad);

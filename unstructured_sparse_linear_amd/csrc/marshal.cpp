@@ -61,6 +61,15 @@ int64_t leading(const at::Tensor& t, const char* name) {
   return t.stride(0);
 }
 
+// Whether two matrices with unit stride along their rows may share memory.
+bool spans_meet(const at::Tensor& a, int64_t lda, const at::Tensor& b, int64_t ldb) {
+  if (a.numel() == 0 || b.numel() == 0) return false;
+  const auto end = [](const at::Tensor& t, int64_t ld) {
+    return (const char*)t.data_ptr() + ((t.size(0) - 1) * ld + t.size(1)) * t.element_size();
+  };
+  return (const char*)a.data_ptr() < end(b, ldb) && (const char*)b.data_ptr() < end(a, lda);
+}
+
 void contiguous(const at::Tensor& t, const char* name) {
   need(t.layout() == at::kStrided && t.is_contiguous(), name, "must be contiguous");
 }
@@ -177,8 +186,9 @@ struct LowRank {
     if (d.scale) same_device(THPVariable_Unpack(v[6]), "scale", dev);
     if (d.ranks) same_device(THPVariable_Unpack(v[7]), "ranks", dev);
   }
-  at::Tensor workspace(spops_low_rank_op op, size_t& bytes) const {
-    status("spops_low_rank_workspace_size", spops_low_rank_workspace_size(&d, op, &bytes));
+  at::Tensor workspace(int op, size_t& bytes) const {
+    status("spops_low_rank_workspace_size",
+           spops_low_rank_workspace_size(&d, (spops_low_rank_op)op, &bytes));
     return bytes ? at::empty({(int64_t)bytes}, xt.options().dtype(at::kByte)) : at::Tensor();
   }
 };
@@ -207,13 +217,16 @@ PyObject* low_rank_forward(PyObject* const* args, Py_ssize_t n, bool project) {
     const c10::DeviceGuard guard(L.xt.device());
     at::Tensor out = into ? THPVariable_Unpack(args[8])
                           : at::empty({L.d.out_features, L.d.tokens}, L.xt.options());
+    const int64_t ldo = leading(out, "out");
+    const bool over_x = into && spans_meet(out, ldo, L.xt, L.ldx);
     size_t bytes = 0;
-    const at::Tensor ws =
-        L.workspace(project ? SPOPS_LOW_RANK_PROJECT : SPOPS_LOW_RANK_ADD, bytes);
+    const at::Tensor ws = L.workspace((project ? SPOPS_LOW_RANK_PROJECT : SPOPS_LOW_RANK_ADD) |
+                                          (over_x ? SPOPS_LOW_RANK_OVER_X : 0),
+                                      bytes);
     const auto call = project ? spops_low_rank_project : spops_low_rank_add;
     status(project ? "spops_low_rank_project" : "spops_low_rank_add",
            call(&L.d, L.first.data_ptr(), L.ldf, L.xt.data_ptr(), L.ldx, out.data_ptr(),
-                leading(out, "out"), ws.defined() ? ws.data_ptr() : nullptr, bytes, stream_of(L.xt.device())));
+                ldo, ws.defined() ? ws.data_ptr() : nullptr, bytes, stream_of(L.xt.device())));
     if (into) {
       written(out);
       Py_INCREF(args[8]);

@@ -685,7 +685,8 @@ def low_rank_add(yt: torch.Tensor, xt: torch.Tensor, A: torch.Tensor, B: torch.T
       scale [adapters]: float32
 
     All matrices share a dtype (f32, f16, bf16); sums are fp32, one rounding.
-    `out` may be yt.  Not differentiable by itself: see LowRankAdapters."""
+    `out` may be yt, and may share memory with xt (yt may be xt too); it overlaps
+    no other input.  Not differentiable by itself: see LowRankAdapters."""
     return _marshal().low_rank_add(yt, xt, A, B, offsets, adapter, scale, ranks, out)
 
 
@@ -696,7 +697,7 @@ def low_rank_project(W: torch.Tensor, xt: torch.Tensor, A: torch.Tensor, B: torc
     """W xt + the requests' adapters in one pass over W (low_rank_add has the
     other arguments): for the few tokens of a decode step.  Correct for any
     number of tokens; for prompts a dense product and low_rank_add are
-    faster."""
+    faster.  `out` may share memory with xt."""
     return _marshal().low_rank_project(W, xt, A, B, offsets, adapter, scale, ranks, out)
 
 
