@@ -507,10 +507,11 @@ spops_status spops_low_rank_backward(const spops_low_rank* L, const void* dyt, i
  * norm = sqrt(sum over all tensors of grad^2) (fp64 sums, one f32 written at
  * `norm`, device memory), c = min(1, max_norm / (norm + 1e-6)), and
  * out[i] = c grad[i] in each tensor's dtype (fp32 product, one rounding).  out may be
- * grad (in place; nothing is written where c is 1).  A norm that is NaN makes
- * every value NaN.  `tensors` is a HOST array, read before the call returns;
- * at most 2^20 tensors of at most 2^36 elements.  max_norm >= 0 (infinity
- * allowed: the norm alone).  Outputs must not overlap other tensors' grads. */
+ * grad (in place; nothing is written where c is 1).  max_norm >= 0.  An infinite
+ * max_norm asks for the norm alone: c is 1 whatever the norm is.  Under a finite
+ * one a norm that is NaN makes every value NaN, and an infinite norm gives c = 0.
+ * `tensors` is a HOST array, read before the call returns; at most 2^20 tensors
+ * of at most 2^36 elements.  Outputs must not overlap other tensors' grads. */
 typedef struct spops_clip_tensor {
   const void* grad;
   void* out;

@@ -1,7 +1,8 @@
 // clip.hip -- the norm of many gradients together, and clipping by it.
 //
 //   norm = sqrt(sum over all tensors of g^2),  c = min(1, max_norm / (norm + 1e-6)),
-//   out = c g   (in place, or into other tensors; a NaN norm gives NaN)
+//   out = c g   (in place, or into other tensors; a NaN norm gives NaN; an
+//                infinite max_norm gives c = 1 whatever the norm)
 //
 // Two launches for up to 250 tensors (and two more for each further 250): the
 // squares' sums, one per workgroup; then every workgroup adds those sums in
@@ -193,7 +194,8 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(const Outs outs, c
   const double norm = sqrt(block_sum(s, red));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
   const double q = max_norm / (norm + 1e-6);
-  const float coef = q > 1.0 ? 1.f : (float)q;
+  // without a limit nothing changes, also where the norm is infinite or NaN
+  const float coef = q > 1.0 || isinf(max_norm) ? 1.f : (float)q;
   while (b < chunks) {
     const void* g = t.grad[p.tensor];
     void* out = outs.out[p.tensor];
