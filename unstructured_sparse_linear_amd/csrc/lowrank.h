@@ -81,6 +81,23 @@ __device__ __forceinline__ void mask8(Frag<T>& f, uint32_t m) {
   }
 }
 
+// Infinities and NaN made finite where `on` (infinity: one of its sign), other
+// values as they are.  The addition carries an exponent of ones into the sign's
+// place, from where it clears the exponent's highest bit: four instructions per
+// pair and no branch, which would cut the schedule of the products around it.
+__device__ __forceinline__ uint32_t exponent_ones(bf16_t*) { return 0x7f807f80u; }
+__device__ __forceinline__ uint32_t exponent_ones(_Float16*) { return 0x7c007c00u; }
+template <typename T>
+__device__ __forceinline__ Frag<T> made_finite(Frag<T> f, bool on) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t ones = exponent_ones((T*)nullptr), lowest = ones & ~(ones << 1);
+    const uint32_t look = on ? ones : 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.w[i] &= ~((((f.w[i] & look) + lowest) >> 1) & 0x40004000u);
+  }
+  return f;
+}
+
 // V consecutive elements of one row of a matrix whose rows run along k.
 template <typename T, int V>
 struct Row {
@@ -127,7 +144,9 @@ __device__ __forceinline__ Frag<T> column(const Row<T, V> (&r)[8], int j) {
 // second product sees 16 (bf16) to 22 (f16) bits of u and the result's one
 // rounding is the output's.  f16 has a narrow exponent range: its operand is
 // scaled by a power of two that brings the largest |u| near one, and the fp32
-// result is scaled back.
+// result is scaled back.  The other operand meets hi as it is and lo with its
+// infinities and NaN made finite: infinity times u is infinity times hi, whose
+// sign is u's, and a lo that is zero or of the other sign must not turn it into NaN.
 
 // hi or lo of u (one element's bits).  bf16: hi truncates, so it never
 // overflows; the remainder is exact and rounded once.  A non-finite u goes

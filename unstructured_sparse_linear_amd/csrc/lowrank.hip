@@ -561,31 +561,47 @@ __device__ __forceinline__ Frag<T> u_frag(const float* row, int step, bool lo, f
   return split8<T>(v, lo);
 }
 
+// A factor's fragment as hi and lo meet it.  SMALL: one fragment for both, the
+// lanes of the block's upper half for lo.
+template <typename T, bool SMALL>
+struct Halves {
+  Frag<T> hi, lo;
+  __device__ __forceinline__ explicit Halves(const Frag<T>& f)
+      : hi(SMALL ? made_finite(f, lane_id() >= 32) : f), lo(SMALL ? hi : made_finite(f, true)) {}
+};
+
 // c + F u for one K block: result rows are F's, columns are u's tokens.
 template <typename T, bool SMALL>
-__device__ __forceinline__ f32x4 u_mma(const Frag<T>& f, const Frag<T>& hi, const Frag<T>& lo,
-                                       f32x4 c) {
+__device__ __forceinline__ f32x4 u_mma(const Halves<T, SMALL>& f, const Frag<T>& hi,
+                                       const Frag<T>& lo, f32x4 c) {
   if constexpr (SMALL && sizeof(T) == 4) {
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(f.w[s]), __uint_as_float(hi.w[s]),
-                                               c, 0, 0, 0);
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(f.hi.w[s]),
+                                               __uint_as_float(hi.w[s]), c, 0, 0, 0);
     return c;
   } else {
-    c = mma(f, hi, c);
-    if constexpr (!SMALL && sizeof(T) == 2) c = mma(f, lo, c);
+    c = mma(f.hi, hi, c);
+    if constexpr (!SMALL && sizeof(T) == 2) c = mma(f.lo, lo, c);
     return c;
   }
 }
 
 // The same turned: rows are u's tokens.
 template <typename T, bool SMALL>
-__device__ __forceinline__ f32x4 token_mma(const Frag<T>& hi, const Frag<T>& lo, const Frag<T>& f,
-                                           f32x4 c) {
-  if constexpr (SMALL && sizeof(T) == 4) return u_mma<T, true>(hi, f, f, c);
-  c = mma(hi, f, c);
-  if constexpr (!SMALL && sizeof(T) == 2) c = mma(lo, f, c);
-  return c;
+__device__ __forceinline__ f32x4 token_mma(const Frag<T>& hi, const Frag<T>& lo,
+                                           const Halves<T, SMALL>& f, f32x4 c) {
+  if constexpr (SMALL && sizeof(T) == 4) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(hi.w[s]),
+                                               __uint_as_float(f.hi.w[s]), c, 0, 0, 0);
+    return c;
+  } else {
+    c = mma(hi, f.hi, c);
+    if constexpr (!SMALL && sizeof(T) == 2) c = mma(lo, f.lo, c);
+    return c;
+  }
 }
 
 // Fragment of B_ad's row o: ranks from rank_base, zero from the adapter's rank
@@ -729,8 +745,9 @@ struct UOperand {
     }
   }
   // acc[q] += f u_q for block k (not yet scaled by up)
-  __device__ __forceinline__ void product(int k, const Frag<T>& f, f32x4 (&acc)[V]) const {
+  __device__ __forceinline__ void product(int k, const Frag<T>& factor, f32x4 (&acc)[V]) const {
     const int g = lane_id() / 16;
+    const Halves<T, SMALL> f(factor);
 #pragma unroll
     for (int q = 0; q < V; ++q) {
       Frag<T> h, l;
@@ -1063,21 +1080,23 @@ __device__ __forceinline__ void outer_tile(const LowRankArgs& a, bool is_x, int6
           }
         }
 #pragma unroll
-        for (int q = 0; q < NR; ++q)
+        for (int k = 0; k < FF; ++k) {
+          const Halves<T, false> h(x[k]);
 #pragma unroll
-          for (int k = 0; k < FF; ++k) {
+          for (int q = 0; q < NR; ++q) {
             f32x4& d = acc[k * NR + q];
             if constexpr (F16) {
               const float up = __uint_as_float(b.e[p][q] << 23);
-              const f32x4 c = mma(x[k], b.lo[p][q],
-                                  mma(x[k], b.hi[p][q], f32x4{0.f, 0.f, 0.f, 0.f}));
+              const f32x4 c = mma(h.lo, b.lo[p][q],
+                                  mma(h.hi, b.hi[p][q], f32x4{0.f, 0.f, 0.f, 0.f}));
 #pragma unroll
               for (int i = 0; i < 4; ++i) d[i] = __builtin_fmaf(c[i], up, d[i]);
             } else {
-              d = mma(x[k], b.hi[p][q], d);
-              if constexpr (HALVES) d = mma(x[k], b.lo[p][q], d);
+              d = mma(h.hi, b.hi[p][q], d);
+              if constexpr (HALVES) d = mma(h.lo, b.lo[p][q], d);
             }
           }
+        }
       }
     };
     if (wave * P < count) load(wave * P, nxt);
@@ -1281,7 +1300,8 @@ __global__ __launch_bounds__((kProjectWaves + V) * kWave) void lowrank_project_k
 #pragma unroll
         for (int d = 0; d < D; ++d)
 #pragma unroll
-          for (int m = 0; m < MO; ++m) c[m][d] = token_mma<T, SMALL>(hi, lo, f[m][d], c[m][d]);
+          for (int m = 0; m < MO; ++m)
+            c[m][d] = token_mma<T, SMALL>(hi, lo, Halves<T, SMALL>(f[m][d]), c[m][d]);
       }
 #pragma unroll
       for (int d = 0; d < D; ++d)
@@ -1482,7 +1502,7 @@ __global__ __launch_bounds__(kFewThreads) void lowrank_few_kernel(LowRankArgs a)
   const Pow2 p = row_pow2<T>(row, a.R);
   const Frag<T> hi = u_frag<T, SMALL>(row, 0, false, p.down);
   const Frag<T> lo = u_frag<T, SMALL>(row, 0, true, p.down);
-  const f32x4 c = u_mma<T, SMALL>(fb, hi, lo, f32x4{0.f, 0.f, 0.f, 0.f});
+  const f32x4 c = u_mma<T, SMALL>(Halves<T, SMALL>(fb), hi, lo, f32x4{0.f, 0.f, 0.f, 0.f});
   if (n < a.T) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
