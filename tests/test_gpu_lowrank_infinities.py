@@ -124,3 +124,30 @@ def test_values_that_split(shape, dt):
     c.B[:, 9, 0] = -INF
     c.A[:, 4, 11] = INF
     classes(c)
+
+
+@pytest.mark.parametrize("shape", ["one-token", "decode", "decode-33-ranks", "prompts",
+                                   "prompts-24-ranks", "prompts-100-ranks"])
+def test_f16_infinite_rank_beside_large_ones(shape):
+    """An infinite u beside finite ones outside f16's range, which keep their
+    sign and size: the scale is that of the finite ones."""
+    c = integers("f16", *SHAPES[shape])
+    c.xt.fill_(300.0)
+    c.A.fill_(200.0)  # u about 1.4e6
+    c.A[:, 3, 5] = INF
+    c.B.fill_(-1.0)
+    c.B[:, :, 3] = 1.0
+    want = S.low_rank_add(c.yt, *c.args())
+    busy = torch.zeros(c.T, dtype=torch.bool, device="cuda")
+    for t, _, _, _ in c.runs():
+        busy[t] = True
+    assert (want[:, busy] == INF).all() and torch.equal(want[:, ~busy], c.yt[:, ~busy])
+    # du beside it: B's infinity in one rank, dx = A^T du with opposite signs
+    c = integers("f16", *SHAPES[shape])
+    c.dyt.fill_(300.0)
+    c.B.fill_(200.0)
+    c.B[:, 3, 2] = INF
+    c.A.fill_(-1.0)
+    c.A[:, 2] = 1.0
+    dx, dA, _ = S.low_rank_backward(c.dyt, *c.args())
+    assert (dx[:, busy] == INF).all() and not dx[:, ~busy].any()

@@ -152,7 +152,7 @@ __device__ __forceinline__ Frag<T> column(const Row<T, V> (&r)[8], int j) {
 // once: hi and lo fill the two halves of the 32-wide K block), so that the
 // second product sees 16 (bf16) to 22 (f16) bits of u and the result's one
 // rounding is the output's.  f16 has a narrow exponent range: its operand is
-// scaled by a power of two that brings the largest |u| near one, and the fp32
+// scaled by a power of two that brings the largest finite |u| near one, and the fp32
 // result is scaled back.  The other operand meets hi as it is and lo with its
 // infinities and NaN made finite: infinity times u is infinity times hi, whose
 // sign is u's, and a lo that is zero or of the other sign must not turn it into NaN.
@@ -189,13 +189,21 @@ __device__ __forceinline__ Frag<T> split8(const float (&u)[8], bool lo) {
   return f;
 }
 
-// 2^-e and 2^e for the exponent e of m = max |u| (finite; otherwise 1 and 1).
+// The larger of m and |u|, or m where u is infinite or NaN: finite values keep
+// their range beside it.
+constexpr float kMaxFloat = 3.402823466e38f;
+__device__ __forceinline__ float max_finite(float m, float u) {
+  u = fabsf(u);
+  return u > m && u <= kMaxFloat ? u : m;
+}
+
+// 2^-e and 2^e for the exponent e of m, the largest finite |u|.
 struct Pow2 {
   float down, up;
 };
 __device__ __forceinline__ Pow2 pow2_of(float m) {
   uint32_t b = (__float_as_uint(m) >> 23) & 255u;
-  b = b == 255u ? 127u : b < 2u ? 2u : b > 252u ? 252u : b;
+  b = b < 2u ? 2u : b > 252u ? 252u : b;
   Pow2 p;
   p.down = __uint_as_float((254u - b) << 23);
   p.up = __uint_as_float(b << 23);

@@ -435,6 +435,10 @@ __global__ __launch_bounds__(kThreads) void lowrank_pack_kernel(LowRankArgs a, i
       if (tid < TT) {
         float m = 0.f;
         for (int r = 0; r < R; ++r) m = fmaxf(m, fabsf(us[r * LD + tid]));
+        if (m > kMaxFloat) {
+          m = 0.f;
+          for (int r = 0; r < R; ++r) m = max_finite(m, us[r * LD + tid]);
+        }
         const Pow2 p = pow2_of(m);
         down[tid] = p.down;
         a.up[t0 + tid] = p.up;
@@ -481,7 +485,7 @@ __global__ __launch_bounds__(kThreads) void lowrank_pack_kernel(LowRankArgs a, i
           uint32_t rest = (uint32_t)__ballot(ad >= 0);
           while (rest) {
             const bool same = ad == __shfl(ad, __builtin_ctz(rest), kWave);
-            float m = same ? fabsf(v) : 0.f;
+            float m = same ? max_finite(0.f, v) : 0.f;
 #pragma unroll
             for (int o = 1; o < TT; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
             big = same ? m : big;
@@ -532,7 +536,7 @@ __device__ __forceinline__ Pow2 row_pow2(const float* row, int R) {
     float m = 0.f;
     for (int r = g * 4; r < staged_width(R) - 4; r += 16)
 #pragma unroll
-      for (int s = 0; s < 4; ++s) m = fmaxf(m, fabsf(row[r + s]));
+      for (int s = 0; s < 4; ++s) m = max_finite(m, row[r + s]);
     m = fmaxf(m, __shfl_xor(m, 16, kWave));
     m = fmaxf(m, __shfl_xor(m, 32, kWave));
     return pow2_of(m);
