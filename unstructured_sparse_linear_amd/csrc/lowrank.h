@@ -159,7 +159,7 @@ __device__ __forceinline__ Frag<T> column(const Row<T, V> (&r)[8], int j) {
 
 // hi or lo of u (one element's bits).  bf16: hi truncates, so it never
 // overflows; the remainder is exact and rounded once.  A non-finite u goes
-// into hi alone.
+// into hi alone.  f16: under 2^-25 of the largest, u counts as zero.
 __device__ __forceinline__ uint32_t split_bits(float u, bool lo, bf16_t*) {
   const uint32_t hb = __float_as_uint(u) & 0xffff0000u;
   if (!lo) return (__float_as_uint(u) & 0x7fffffffu) > 0x7f800000u ? 0x7fc0u : hb >> 16;
