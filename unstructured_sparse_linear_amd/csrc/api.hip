@@ -942,10 +942,10 @@ spops_status low_rank_args(const spops_low_rank* L, int op, const void* second, 
   if (ldx < L->tokens || ldo < L->tokens) return SPOPS_ERR_SHAPE;
   if (op != kLowRankProject && lds < L->tokens) return SPOPS_ERR_SHAPE;
   if (op == kLowRankProject && lds < L->in_features) return SPOPS_ERR_SHAPE;
-  // one launch covers the token tiles times the row blocks
+  // workgroups are counted in 32 bits: the token tiles times the row blocks
   const int64_t widest = std::max(L->out_features, L->in_features);
   if ((L->tokens / 16 + 1) * (widest / 16 + 1) > INT32_MAX) return SPOPS_ERR_SHAPE;
-  // and the gradients' the factors' rows
+  // and for the gradients the factors' rows times the pool
   if (op == kLowRankBackward &&
       ((L->in_features + L->out_features) / 32 + 2) * L->adapters * ((L->rank + 63) / 64) +
               (L->tokens / 64 + 1) * (widest / 64 + 1) > INT32_MAX)
@@ -958,6 +958,7 @@ spops_status low_rank_args(const spops_low_rank* L, int op, const void* second, 
                         L->dtype == SPOPS_F32 ? 4 : 2);
     const LowRankLayout l = lowrank_layout(op, over_x, L->dtype, L->tokens, L->requests,
                                            L->adapters, L->rank, L->in_features, L->out_features);
+    if (l.shrink_blocks > INT32_MAX) return SPOPS_ERR_SHAPE;
     if (l.bytes > 0 && (!workspace || bytes < l.bytes || ((uintptr_t)workspace & 255)))
       return SPOPS_ERR_WORKSPACE;
   }

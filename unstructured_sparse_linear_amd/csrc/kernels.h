@@ -411,6 +411,7 @@ struct LowRankArgs {
   const int32_t* adapter;  // [S]
   const int32_t* ranks;    // [n] or null (R)
   const float* scale;      // [n] or null (1)
+  uint32_t block0, blocks; // the launch's first workgroup, and those of all its parts
   // filled from the workspace by launch_lowrank
   int64_t Tp;              // row length of u and du
   int32_t* tokad;          // [Tp] adapter of each token, -1 for none
@@ -431,6 +432,7 @@ struct LowRankLayout {
   int groups;              // workgroups that share a tile's adapters
   int slices_u, slices_du; // slices of the features
   bool few;                // one launch, which reads x while it writes out
+  int64_t shrink_blocks;   // workgroups of the shrink kernel
   size_t at_tokad, at_u, at_du, at_packed, at_rows, at_up, at_ru, at_rdu, at_eu, at_edu, bytes;
 };
 // over_x: out shares memory with x (only where op is not backward).

@@ -51,6 +51,8 @@ __device__ __forceinline__ uint32_t xcd_chunk(uint32_t b, uint32_t N) {
   return x * q + (x < r ? x : r) + b / 8;
 }
 
+__device__ __forceinline__ uint32_t block_of(const LowRankArgs& a) { return a.block0 + blockIdx.x; }
+
 // ------------------------------------------------------ adapters of tokens --
 
 template <int TT>
@@ -387,7 +389,7 @@ __global__ __launch_bounds__(kThreads, V * NR >= 8 ? 2 : 3) void lowrank_shrink_
   __shared__ TokenTile<16 * V> tile;
   // tiles are the fastest index, then the parts of a tile, then the slices
   const int tiles = (int)((a.T + 16 * V - 1) / (16 * V)), parts = groups * ((a.R + 63) / 64);
-  const uint32_t b = xcd_chunk(blockIdx.x, gridDim.x);
+  const uint32_t b = xcd_chunk(block_of(a), a.blocks);
   const int tile_id = b % tiles, part = b / tiles % parts, z = b / tiles / parts;
   if (!BACKWARD || z < jx.slices)
     shrink_tile<T, V, NR, false, PACK>(a, jx, z, tile_id, part, b < (uint32_t)tiles, groups, red,
@@ -419,7 +421,7 @@ __global__ __launch_bounds__(kThreads) void lowrank_pack_kernel(LowRankArgs a, i
   const bool is_du = BACKWARD && blockIdx.y == 1;
   const float* u = is_du ? a.du : a.u;
   const int slices = is_du ? sd : su, tid = threadIdx.x, R = a.R;
-  const int64_t t0 = (int64_t)blockIdx.x * TT, size = (int64_t)R * a.Tp;
+  const int64_t t0 = (int64_t)block_of(a) * TT, size = (int64_t)R * a.Tp;
   for (int i = tid; i < R * (TT / 4); i += kThreads) {
     const int r = i / (TT / 4), t = i % (TT / 4) * 4;
     const float* p = u + (int64_t)r * a.Tp + t0 + t;
@@ -917,7 +919,7 @@ __global__ __launch_bounds__(kThreads, (expand_waves<T, V, STEPS, SMALL>())) voi
   constexpr int TT = 16 * V;
   extern __shared__ __attribute__((aligned(16))) char operand[];
   __shared__ TileAdapters<TT> tile;
-  const uint32_t b = xcd_chunk(blockIdx.x, gridDim.x);
+  const uint32_t b = xcd_chunk(block_of(a), a.blocks);
   const int64_t t0 = (int64_t)(b % tiles) * TT, row0 = (int64_t)(b / tiles) * rows_per_block;
   const int64_t end = row0 + rows_per_block < a.n_out ? row0 + rows_per_block : a.n_out;
   if constexpr (V == 1)
@@ -1151,14 +1153,16 @@ __global__ __launch_bounds__(kThreads, 3) void lowrank_gradients_kernel(LowRankA
   } sh;
   const int rcs = (a.R + 63) / 64;
   const int64_t outer = (int64_t)(xblocks + yblocks) * a.n * rcs;
-  if (blockIdx.x < outer) {
-    const uint32_t b = xcd_chunk(blockIdx.x, (uint32_t)outer);
+  const uint32_t block = block_of(a);
+  if (block < outer) {
+    const uint32_t b = xcd_chunk(block, (uint32_t)outer);
     const int per = a.n * rcs, fb = b / per, rest = b % per;
     const bool is_x = fb < xblocks;
     outer_tile<T, NR, FF>(a, is_x, (int64_t)(is_x ? fb : fb - xblocks) * (16 * FF), rest / rcs,
                       rest % rcs * 64, sh.outer);
   } else {
-    const int64_t b = xcd_chunk(blockIdx.x - outer, gridDim.x - outer), t0 = b % tiles * TT, row0 = b / tiles * rows_per_block;
+    const int64_t b = xcd_chunk(block - outer, a.blocks - outer), t0 = b % tiles * TT,
+                  row0 = b / tiles * rows_per_block;
     const int64_t end = row0 + rows_per_block < a.n_in ? row0 + rows_per_block : a.n_in;
     if constexpr (!SMALL) copy_rows<V, kThreads>(a, t0, operand);
     tile_adapters<TT, kThreads>(a, t0, __is_same(T, _Float16), sh.tile);
@@ -1181,8 +1185,8 @@ __global__ __launch_bounds__((kProjectWaves + V) * kWave) void lowrank_project_k
   __shared__ f32x4 red[(kProjectWaves + 1) * MO * V * kWave];
   const int lane = lane_id(), n = lane % 16, g = lane / 16;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int block = blockIdx.x % row_blocks;
-  const int64_t tile = blockIdx.x / row_blocks;
+  const int block = block_of(a) % row_blocks;
+  const int64_t tile = block_of(a) / row_blocks;
   int64_t t0 = tile * TT;
   if (t0 > a.T - TT) t0 = a.T > TT ? a.T - TT : 0;
   const int64_t lim = a.T - V, o0 = (int64_t)block * (16 * MO);
@@ -1560,17 +1564,31 @@ int slices_for(double blocks, int64_t K) {
   return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
 }
 
+// launch(arguments, grid) for workgroups of `threads`.  A launch has fewer than
+// 2^32 work-items; what is more goes into further ones.  Parts of whole rounds over
+// the XCDs keep each XCD's share together.
+template <typename F>
+hipError_t in_parts(LowRankArgs a, int64_t blocks, int threads, F launch) {
+  const int64_t most = (int64_t)(UINT32_MAX / (uint32_t)threads) / 8 * 8;
+  a.blocks = (uint32_t)blocks;
+  for (int64_t b = 0; b < blocks; b += most) {
+    a.block0 = (uint32_t)b;
+    launch(a, (unsigned)(blocks - b < most ? blocks - b : most));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <typename T, int V, bool BACKWARD, bool PACK>
 hipError_t shrink_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
-  const int rcs = (int)cdiv(a.R, 64);
   ShrinkJob jx{a.x, a.A, a.u, a.ldx, a.n_in, l.slices_u};
   ShrinkJob jy{a.y, a.B, a.du, a.ldy, a.n_out, l.slices_du};
-  const dim3 grid((unsigned)(cdiv(a.T, 16 * V) * l.groups * rcs *
-                             (l.slices_u + (BACKWARD ? l.slices_du : 0))));
   auto launch = [&](auto ranks) {
-    hipLaunchKernelGGL((lowrank_shrink_kernel<T, V, decltype(ranks)::value, BACKWARD, PACK>), grid,
-                       dim3(kThreads), 0, s, a, jx, jy, l.groups);
-    return hipGetLastError();
+    return in_parts(a, l.shrink_blocks, kThreads, [&](const LowRankArgs& p, unsigned grid) {
+      hipLaunchKernelGGL((lowrank_shrink_kernel<T, V, decltype(ranks)::value, BACKWARD, PACK>),
+                         dim3(grid), dim3(kThreads), 0, s, p, jx, jy, l.groups);
+    });
   };
   if (a.R <= 16) return launch(Int<1>{});
   if (a.R <= 32) return launch(Int<2>{});
@@ -1613,30 +1631,29 @@ bool packs(int op, int64_t T, int64_t S) {
 
 template <typename T, bool BACKWARD>
 hipError_t pack(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
-  const dim3 grid((unsigned)(a.Tp / kPackTokens), BACKWARD ? 2 : 1);
-  hipLaunchKernelGGL((lowrank_pack_kernel<T, BACKWARD>), grid, dim3(kThreads),
-                     (size_t)a.R * (kPackTokens + 1) * 4, s, a, l.slices_u, l.slices_du);
-  return hipGetLastError();
+  return in_parts(a, a.Tp / kPackTokens, kThreads, [&](const LowRankArgs& p, unsigned grid) {
+    hipLaunchKernelGGL((lowrank_pack_kernel<T, BACKWARD>), dim3(grid, BACKWARD ? 2 : 1),
+                       dim3(kThreads), (size_t)a.R * (kPackTokens + 1) * 4, s, p, l.slices_u,
+                       l.slices_du);
+  });
 }
 
 template <typename T, int V>
 hipError_t expand_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
   const int64_t tiles = cdiv(a.T, 16 * V), per = rows_per_block(a.n_out, tiles);
-  const dim3 grid((unsigned)(cdiv(a.n_out, per) * tiles));
-  const size_t lds = operand_bytes<V>(a.R);
-  if (a.R <= 16)
-    hipLaunchKernelGGL((lowrank_expand_kernel<T, V, 1, true>), grid, dim3(kThreads), lds, s, a,
-                       l.slices_u, (int)tiles, (int)per);
-  else if (a.R <= 32)
-    hipLaunchKernelGGL((lowrank_expand_kernel<T, V, 1, false>), grid, dim3(kThreads), lds, s, a,
-                       l.slices_u, (int)tiles, (int)per);
-  else if (a.R <= 64)
-    hipLaunchKernelGGL((lowrank_expand_kernel<T, V, 2, false>), grid, dim3(kThreads), lds, s, a,
-                       l.slices_u, (int)tiles, (int)per);
-  else
-    hipLaunchKernelGGL((lowrank_expand_kernel<T, V, 0, false>), grid, dim3(kThreads), lds, s, a,
-                       l.slices_u, (int)tiles, (int)per);
-  return hipGetLastError();
+  auto launch = [&](auto steps, auto small) {
+    return in_parts(a, cdiv(a.n_out, per) * tiles, kThreads,
+                    [&](const LowRankArgs& p, unsigned grid) {
+      hipLaunchKernelGGL((lowrank_expand_kernel<T, V, decltype(steps)::value,
+                                                decltype(small)::value != 0>),
+                         dim3(grid), dim3(kThreads), operand_bytes<V>(a.R), s, p, l.slices_u,
+                         (int)tiles, (int)per);
+    });
+  };
+  if (a.R <= 16) return launch(Int<1>{}, Int<1>{});
+  if (a.R <= 32) return launch(Int<1>{}, Int<0>{});
+  if (a.R <= 64) return launch(Int<2>{}, Int<0>{});
+  return launch(Int<0>{}, Int<0>{});
 }
 
 template <typename T, int FF>
@@ -1644,14 +1661,15 @@ hipError_t gradients_f(const LowRankArgs& a, hipStream_t s) {
   constexpr int TT = 256 / sizeof(T);
   const int64_t xb = cdiv(a.n_in, 16 * FF), yb = cdiv(a.n_out, 16 * FF);
   const int64_t tiles = cdiv(a.T, TT), per = rows_per_block(a.n_in, tiles > 0 ? tiles : 1);
-  const dim3 grid((unsigned)((xb + yb) * a.n * cdiv(a.R, 64) + cdiv(a.n_in, per) * tiles));
+  const int64_t blocks = (xb + yb) * a.n * cdiv(a.R, 64) + cdiv(a.n_in, per) * tiles;
   const size_t lds = operand_bytes<16 / sizeof(T)>(a.R);
   const int t = (int)(tiles > 0 ? tiles : 1);
   auto launch = [&](auto nr, auto steps, auto small) {
-    hipLaunchKernelGGL((lowrank_gradients_kernel<T, decltype(nr)::value, decltype(steps)::value,
-                                                 decltype(small)::value != 0, FF>),
-                       grid, dim3(kThreads), lds, s, a, (int)xb, (int)yb, t, (int)per);
-    return hipGetLastError();
+    return in_parts(a, blocks, kThreads, [&](const LowRankArgs& p, unsigned grid) {
+      hipLaunchKernelGGL((lowrank_gradients_kernel<T, decltype(nr)::value, decltype(steps)::value,
+                                                   decltype(small)::value != 0, FF>),
+                         dim3(grid), dim3(kThreads), lds, s, p, (int)xb, (int)yb, t, (int)per);
+    });
   };
   if (a.R <= 16) return launch(Int<1>{}, Int<1>{}, Int<1>{});
   if constexpr (FF > 2) return launch(Int<2>{}, Int<1>{}, Int<0>{});
@@ -1675,15 +1693,15 @@ hipError_t gradients(const LowRankArgs& a, hipStream_t s) {
 template <typename T, int V, int MO>
 hipError_t project_vm(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s) {
   const int64_t rb = cdiv(a.n_out, 16 * MO);
-  const dim3 grid((unsigned)(rb * cdiv(a.T, 16 * V))), block((kProjectWaves + V) * kWave);
-  const size_t lds = staged_bytes(16 * V, a.R);
-  if (a.R <= 16)
-    hipLaunchKernelGGL((lowrank_project_kernel<T, V, MO, true>), grid, block, lds, s, a, l.slices_u,
-                       (int)rb);
-  else
-    hipLaunchKernelGGL((lowrank_project_kernel<T, V, MO, false>), grid, block, lds, s, a,
-                       l.slices_u, (int)rb);
-  return hipGetLastError();
+  constexpr int threads = (kProjectWaves + V) * kWave;
+  auto launch = [&](auto small) {
+    return in_parts(a, rb * cdiv(a.T, 16 * V), threads, [&](const LowRankArgs& p, unsigned grid) {
+      hipLaunchKernelGGL((lowrank_project_kernel<T, V, MO, decltype(small)::value != 0>),
+                         dim3(grid), dim3(threads), staged_bytes(16 * V, a.R), s, p, l.slices_u,
+                         (int)rb);
+    });
+  };
+  return a.R <= 16 ? launch(Int<1>{}) : launch(Int<0>{});
 }
 
 template <typename T, int V>
@@ -1765,6 +1783,7 @@ LowRankLayout lowrank_layout(int op, bool over_x, int dtype, int64_t T, int64_t 
   const double blocks = (double)tiles * busy * (double)cdiv(R, 64) * (op == kLowRankBackward ? 2 : 1);
   l.slices_u = slices_for(blocks, n_in);
   l.slices_du = op == kLowRankBackward ? slices_for(blocks, n_out) : 0;
+  l.shrink_blocks = tiles * l.groups * cdiv(R, 64) * (l.slices_u + l.slices_du);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
