@@ -145,7 +145,9 @@ class LowRankAdapters(torch.nn.Module):
       project(W, xt, offsets, adapter)    W xt + the same in one pass over W,
                                           for decode steps (no gradient)
 
-    yt may come from any layer on xt, a dense product or a SparseAdapter."""
+    yt may come from any layer on xt, a dense product or a SparseAdapter.  scale
+    and ranks (one value per adapter, of any device and type) are kept as float32
+    and int32 buffers, also where the module is cast."""
 
     def __init__(self, adapters: int, rank: int, in_features: int, out_features: int,
                  scale: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None,
@@ -155,8 +157,19 @@ class LowRankAdapters(torch.nn.Module):
         self.A = torch.nn.Parameter(A.to(dtype))
         self.B = torch.nn.Parameter(torch.zeros(adapters, out_features, rank, dtype=dtype,
                                                 device=device))
-        self.register_buffer("scale", scale)
-        self.register_buffer("ranks", ranks)
+        # the calls take them in these types alone, whatever the factors' dtype
+        self.register_buffer("scale", scale if scale is None else
+                             scale.to(device, torch.float32))
+        self.register_buffer("ranks", ranks if ranks is None else ranks.to(device, torch.int32))
+
+    def _apply(self, fn, *args, **kwargs):
+        """Moves and casts of the module: scale moves, but stays float32 with the
+        values it had."""
+        scale = self.scale
+        super()._apply(fn, *args, **kwargs)
+        if scale is not None and self.scale.dtype != torch.float32:
+            self.scale = scale.to(self.scale.device)
+        return self
 
     def forward(self, yt: torch.Tensor, xt: torch.Tensor, offsets: torch.Tensor,
                 adapter: torch.Tensor) -> torch.Tensor:
