@@ -23,6 +23,7 @@ from __future__ import annotations
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .spops import (SddmmPlan, SpmmPlan, csr_add, csr_transpose_permutation, low_rank_add,
                     low_rank_backward, low_rank_project, masked_adam, permute_values, sddmm,
@@ -117,6 +118,7 @@ class _LowRankLinearFn(torch.autograd.Function):
         return low_rank_add(yt, xt, A, B, offsets, adapter, scale, ranks)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dyt):
         xt, A, B, offsets, adapter, scale, ranks = ctx.saved_tensors
         dx = dA = dB = None
@@ -132,7 +134,7 @@ def low_rank_linear(yt: torch.Tensor, xt: torch.Tensor, A: torch.Tensor, B: torc
                     offsets: torch.Tensor, adapter: torch.Tensor,
                     scale: Optional[torch.Tensor] = None,
                     ranks: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """low_rank_add, differentiable in yt, xt, A and B."""
+    """low_rank_add, differentiable once in yt, xt, A and B."""
     return _LowRankLinearFn.apply(yt, xt, A, B, offsets, adapter, scale, ranks)
 
 
