@@ -66,6 +66,7 @@ class _SparseLinearFn(torch.autograd.Function):
         return yt
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dyt: torch.Tensor):
         values, xt = ctx.saved_tensors
         P = ctx.pattern
