@@ -135,7 +135,10 @@ def low_rank_linear(yt: torch.Tensor, xt: torch.Tensor, A: torch.Tensor, B: torc
                     offsets: torch.Tensor, adapter: torch.Tensor,
                     scale: Optional[torch.Tensor] = None,
                     ranks: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """low_rank_add, differentiable once in yt, xt, A and B."""
+    """low_rank_add, differentiable once in yt, xt, A and B.  scale has no gradient:
+    one that requires it is refused."""
+    if scale is not None and scale.requires_grad and torch.is_grad_enabled():
+        raise ValueError("scale has no gradient; detach it")
     return _LowRankLinearFn.apply(yt, xt, A, B, offsets, adapter, scale, ranks)
 
 
