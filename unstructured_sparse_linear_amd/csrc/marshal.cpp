@@ -278,6 +278,31 @@ struct Sequence {
   PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(seq, i); }
 };
 
+// Whether no output starts where another one or another tensor's gradient does: the
+// same tensor twice, a buffer beside its first slice, outputs in another order.  An
+// open table of the outputs' addresses, under a microsecond for 200 tensors.
+bool apart(const std::vector<spops_clip_tensor>& ts) {
+  size_t size = 16;
+  while (size < 2 * ts.size()) size *= 2;
+  std::vector<int32_t> table(size, -1);
+  const auto slot = [&](const void* p) {
+    size_t at = ((uint64_t)(uintptr_t)p * 0x9e3779b97f4a7c15ull >> 20) & (size - 1);
+    while (table[at] >= 0 && ts[(size_t)table[at]].out != p) at = (at + 1) & (size - 1);
+    return &table[at];
+  };
+  for (size_t i = 0; i < ts.size(); ++i) {
+    if (ts[i].numel == 0) continue;
+    int32_t* s = slot(ts[i].out);
+    if (*s >= 0) return false;
+    *s = (int32_t)i;
+  }
+  for (size_t i = 0; i < ts.size(); ++i) {
+    if (ts[i].numel == 0 || ts[i].grad == ts[i].out) continue;
+    if (*slot(ts[i].grad) >= 0) return false;
+  }
+  return true;
+}
+
 PyObject* clip_grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (!count_args(n, 3)) return nullptr;
   return guarded([&]() -> PyObject* {
@@ -305,6 +330,8 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
         t.out = t.numel ? o.data_ptr() : nullptr;
       }
     }
+    need(apart(ts), into ? "every out" : "every gradient",
+         "must be a tensor of its own, given once");
     const at::Tensor& g0 = THPVariable_Unpack(grads[0]);
     const c10::Device dev = g0.device();
     for (Py_ssize_t i = 0; i < count; ++i) {

@@ -718,7 +718,8 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float,
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)), with norm the
     2-norm over all of them, in place or into the tensors `out`; returns the
     norm (float32, on the device: nothing synchronizes).  Any mix of f32, f16
-    and bf16 tensors.  A NaN norm makes every value NaN; an infinite max_norm
+    and bf16 tensors.  What is written overlaps no other tensor of the call; the
+    same tensor twice is refused.  A NaN norm makes every value NaN; an infinite max_norm
     changes nothing, whatever the norm."""
     return _marshal().clip_grad_norm(grads, max_norm, out)
 
