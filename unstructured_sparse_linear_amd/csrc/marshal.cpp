@@ -310,7 +310,8 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (max_norm == -1.0 && PyErr_Occurred()) throw PythonError{};
     const Sequence grads(args[0], "grads must be a sequence of tensors");
     const bool into = given(args[2]);
-    const Sequence outs(into ? args[2] : args[0], "out must be a sequence of tensors");
+    // one pass over grads: an iterator has no second
+    const Sequence outs(into ? args[2] : grads.seq, "out must be a sequence of tensors");
     const Py_ssize_t count = grads.size();
     need(count > 0, "grads", "must hold at least one tensor");
     need(outs.size() == count, "out", "must have one tensor per gradient");

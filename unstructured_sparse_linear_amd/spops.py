@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 from collections import OrderedDict
-from typing import Optional, Sequence, Tuple
+from typing import Iterable, Optional, Tuple
 
 import torch
 
@@ -713,8 +713,8 @@ def low_rank_backward(dyt: torch.Tensor, xt: torch.Tensor, A: torch.Tensor, B: t
     return _marshal().low_rank_backward(dyt, xt, A, B, offsets, adapter, scale, ranks)
 
 
-def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float,
-                   out: Optional[Sequence[torch.Tensor]] = None) -> torch.Tensor:
+def clip_grad_norm(grads: Iterable[torch.Tensor], max_norm: float,
+                   out: Optional[Iterable[torch.Tensor]] = None) -> torch.Tensor:
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)), with norm the
     2-norm over all of them, in place or into the tensors `out`; returns the
     norm (float32, on the device: nothing synchronizes).  Any mix of f32, f16
