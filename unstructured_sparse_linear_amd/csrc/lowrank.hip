@@ -1771,7 +1771,8 @@ LowRankLayout lowrank_layout(int op, bool over_x, int dtype, int64_t T, int64_t 
                              int64_t R, int64_t n_in, int64_t n_out) {
   LowRankLayout l{};
   l.few = !over_x && few(op, T, S, n, R);
-  if (l.few) return l;  // one launch, nothing between
+  if (l.few) return l;   // one launch, nothing between
+  if (T == 0) return l;  // the gradients' zeros alone
   const int64_t eb = dtype == kF32 ? 4 : 2;
   l.Tp = cdiv(T, 128) * 128;  // whole tiles
   l.width = token_width(op, dtype, T, R);
