@@ -6,7 +6,10 @@
 //
 // Two launches for up to 250 tensors (and two more for each further 250): the
 // squares' sums, one per workgroup; then every workgroup adds those sums in
-// the same order and scales its part, its first values already requested.  The
+// the same order and scales its part, its first values already requested.  More
+// sums than one launch leaves are added once, by a launch between (2000 tensors of
+// 65536 bf16 values: 244 us, 336 where each workgroup adds them; 500 of 1000 values:
+// 22 us, 24 with it).  The
 // tensors' table travels in the kernel arguments, 16 bytes a tensor with the
 // first launch (which leaves it in the workspace for the second) and 8 with the
 // second, so a call copies nothing to the device and may be captured.  Sums are
@@ -175,6 +178,17 @@ __global__ __launch_bounds__(kThreads, 6) void clip_norm_kernel(const Table t, d
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
+// The sum of the workgroups' sums, in the order of clip_scale_kernel's.
+__global__ __launch_bounds__(kThreads) void clip_total_kernel(const double* partial, int partials,
+                                                              double* total) {
+  __shared__ double red[kThreads / kWave];
+  double s = 0.0;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < partials; i += kThreads) s += partial[i];
+  s = block_sum(s, red);
+  if (threadIdx.x == 0) *total = s;
+}
+
 __global__ __launch_bounds__(kThreads) void clip_scale_kernel(const Outs outs, const Table* table,
                                                               const double* partial, int partials,
                                                               double max_norm, float* norm_out) {
@@ -264,6 +278,14 @@ hipError_t launch_clip(const ClipTensor* ts, int64_t count, double max_norm, flo
     hipLaunchKernelGGL(clip_scale_kernel, dim3(1), dim3(kThreads), 0, s, o, (const Table*)nullptr,
                        partial, 0, max_norm, norm);
     return hipGetLastError();
+  }
+  if (partials > kMaxBlocks) {
+    hipLaunchKernelGGL(clip_total_kernel, dim3(1), dim3(kThreads), 0, s, partial, partials,
+                       partial + partials);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    partial += partials;
+    partials = 1;
   }
   launches = 0;
   for (int64_t i = 0; i < count;) {
