@@ -47,3 +47,17 @@ def test_many_in_a_graph():
         assert torch.equal(norm, S.clip_grad_norm(grads, 1.0, out=eager))
         for a, b in zip(eager, outs):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("max_norm", [1e9, 0.5])
+def test_some_in_place(max_norm):
+    """Below the limit what is in place is left alone, and the rest is copied."""
+    grads = make([8192 * 1600, 8192 * 1700 + 5, 8192 * 9, 77], "mixed")
+    kept = [g.clone() for g in grads]
+    outs = [g if i % 2 == 0 else torch.full_like(g, 7.0) for i, g in enumerate(grads)]
+    norm = S.clip_grad_norm(grads, max_norm, out=outs)
+    check(kept, outs, norm, max_norm)
+    assert torch.equal(grads[1], kept[1]) and torch.equal(grads[3], kept[3])
+    if max_norm == 1e9:
+        for o, k in zip(outs, kept):
+            assert torch.equal(o, k)

@@ -223,7 +223,7 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(const Outs outs, c
     b += gridDim.x;
     if (b >= chunks) break;
     p = find_piece(t, chunks - 1 - b);
-    if (p.n == kChunk)
+    if (p.n == kChunk && (coef != 1.f || outs.out[p.tensor] != t.grad[p.tensor]))
       with_type(p.dtype, [&](auto* as) { hold(typed(t.grad[p.tensor], p.at, as), held); });
   }
 }
