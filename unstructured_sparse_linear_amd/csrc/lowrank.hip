@@ -1347,7 +1347,8 @@ constexpr int kFewThreads = 1024;
 constexpr int kFewWaves = kFewThreads / kWave;
 
 // A few tokens with one adapter at most, in one launch: every workgroup makes
-// u = A x for itself, from its XCD's L2 (128 KB for 16 ranks of 4096 features).
+// u = A x for itself, from its XCD's L2 (128 KB for 16 ranks of 4096 features in 16
+// bits; `few` bounds it).
 // add: sixteen waves split A's features, then take 16 rows of B each.  project:
 // a workgroup takes 16 rows of W, whose features eight waves split; the other
 // eight find the adapter and make u and B u meanwhile.
@@ -1715,12 +1716,26 @@ hipError_t project_v(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s
 }
 
 // One launch for up to 16 tokens that cannot have more than one adapter, of up
-// to 32 ranks (a workgroup of project then reads no more of A than twice its
-// rows of W).  One token of 4096 x 4096, 16 ranks, bf16: add 9.2 us where two
-// launches take 13.6, project 13.3 where they take 17.7.  Its workgroups read x
-// while others write: not where out shares memory with x.
-bool few(int op, int64_t T, int64_t S, int64_t n, int64_t R) {
-  return op != kLowRankBackward && T <= kFewTokens && R <= 32 && (T <= 1 || S <= 1 || n <= 1);
+// to 32 ranks, where what every workgroup reads for itself costs less than a second
+// launch.  Its workgroups read x while others write: not where out shares memory
+// with x.  us, one launch and two, one token, bf16:
+//   add: all of A (its ranks rounded up to 16).  16 ranks of 4096 features 9.2 and
+//   10.6, of 4608 10.0 and 10.8, of 6144 11.8 and 10.8, of 11008 17.4 and 11.3;
+//   32 ranks of 2048 9.3 and 10.4, of 4096 13.2 and 11.1.
+//   project: A and 16 rows of W, in as many rounds as the rows take with one such
+//   workgroup a CU, against 48 rows each in the other form.  16 ranks of 4096 x 4096
+//   13.0 and 17.0, of 8192 features 21.6 and 21.9, 4096 features and 11008 rows 34.1
+//   and 27.8, 1024 and 11008 15.1 and 17.6, 4096 and 16384 45.9 and 49.1.  More
+//   tokens read x a value at a time: 16 of 6144 x 4096 21.0 and 19.5, of 2048 x
+//   11008 24.1 and 19.3.
+bool few(int op, int64_t eb, int64_t T, int64_t S, int64_t n, int64_t R, int64_t n_in,
+         int64_t n_out) {
+  if (op == kLowRankBackward || T > kFewTokens || R > 32 || (T > 1 && S > 1 && n > 1)) return false;
+  const int64_t row = n_in * eb, ranks = R <= 16 ? 16 : 32;
+  if (op == kLowRankAdd) return ranks * row <= 144 * 1024;
+  const int64_t rounds = cdiv(n_out, 16 * 256), others = cdiv(n_out, 48 * 256);
+  return (ranks + 16) * row * rounds / others <=
+         (T <= 1 ? 512 : rounds == 1 ? 384 : 288) * 1024;
 }
 
 template <typename T, bool PROJECT>
@@ -1770,10 +1785,10 @@ hipError_t project_t(const LowRankArgs& a, const LowRankLayout& l, hipStream_t s
 LowRankLayout lowrank_layout(int op, bool over_x, int dtype, int64_t T, int64_t S, int64_t n,
                              int64_t R, int64_t n_in, int64_t n_out) {
   LowRankLayout l{};
-  l.few = !over_x && few(op, T, S, n, R);
+  const int64_t eb = dtype == kF32 ? 4 : 2;
+  l.few = !over_x && few(op, eb, T, S, n, R, n_in, n_out);
   if (l.few) return l;   // one launch, nothing between
   if (T == 0) return l;  // the gradients' zeros alone
-  const int64_t eb = dtype == kF32 ? 4 : 2;
   l.Tp = cdiv(T, 128) * 128;  // whole tiles
   l.width = token_width(op, dtype, T, R);
   const int64_t tiles = cdiv(T, 16 * l.width);
