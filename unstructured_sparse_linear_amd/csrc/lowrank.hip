@@ -1673,10 +1673,13 @@ hipError_t gradients_f(const LowRankArgs& a, hipStream_t s) {
     });
   };
   if (a.R <= 16) return launch(Int<1>{}, Int<1>{}, Int<1>{});
-  if constexpr (FF > 2) return launch(Int<2>{}, Int<1>{}, Int<0>{});
-  if (a.R <= 32) return launch(Int<2>{}, Int<1>{}, Int<0>{});
-  if (a.R <= 64) return launch(Int<4>{}, Int<2>{}, Int<0>{});
-  return launch(Int<4>{}, Int<0>{}, Int<0>{});
+  if constexpr (FF > 2) {
+    return launch(Int<2>{}, Int<1>{}, Int<0>{});  // up to 32 ranks
+  } else {
+    if (a.R <= 32) return launch(Int<2>{}, Int<1>{}, Int<0>{});
+    if (a.R <= 64) return launch(Int<4>{}, Int<2>{}, Int<0>{});
+    return launch(Int<4>{}, Int<0>{}, Int<0>{});
+  }
 }
 
 // Features of an outer workgroup: 64 share each load of u where that still
