@@ -797,9 +797,10 @@ __device__ __forceinline__ void load_rows(const T* p, int64_t ld, int64_t ob, in
 }
 
 // expand: out = y + B u (out may be y itself; 8192 tokens x 11008 rows, 16 ranks,
-// bf16: 76 us, 4.7 TB/s, the rate of a copy; 64 ranks: 96 us).  DX: out = A^T du, zero where a
-// token has no adapter.  A workgroup keeps the ranks of 16 V tokens in
-// registers and walks rows of the output, 16 a wave at a time: sixteen lanes
+// bf16: 76 us, 4.7 TB/s; 64 ranks: 95 us).  DX: out = A^T du, zero where a
+// token has no adapter.  A workgroup keeps the ranks of 16 V tokens (in
+// registers up to 16 ranks, past them in shared memory) and walks rows of the
+// output, 16 a wave at a time: sixteen lanes
 // hold 16 V neighbouring tokens of a row (256 bytes), four rows a load.  The
 // next rows' values and factors are requested before the present ones are
 // used.  Distinct adapters are computed for the whole tile one after another
@@ -1537,8 +1538,10 @@ constexpr int64_t kFillBlocks = 512;  // two workgroups on each of the 256 CUs
 // 54 us at 256, 41 at 384, 48 at 512).
 constexpr int64_t kShrinkBlocks = 384;
 
-// Tokens a lane holds of a row in the shrink kernel: 16 bytes a load where the
-// sums' registers leave four waves a SIMD.
+// Tokens a lane holds of a row in the shrink kernel: 16 bytes a load of a 16-bit
+// type up to 32 ranks.  Past them the sums of eight tokens (32 tiles of a 16-row
+// product, four registers each) would leave one wave a SIMD; with four tokens two
+// fit, as with eight up to 32 ranks, and narrower forms leave three.
 int token_width(int op, int dtype, int64_t T, int64_t R) {
   const int most = op == kLowRankProject || dtype == kF32 || R > 32 ? 4 : 8;
   int v = 1;
@@ -1623,8 +1626,8 @@ int64_t rows_per_block(int64_t rows, int64_t tiles) {
 // 16-token tiles without that launch: staged for few tokens, and for some more
 // where most tiles have many adapters (which a wide tile computes one after
 // another).  4096 x 4096, 16 ranks, bf16, staged against packed, us: one request
-// of 128 tokens 13.9 and 17.0, of 192 14.8 and 17.8, of 256 18.1 and 17.6; 256
-// requests of one token 33 and 42.
+// of 128 tokens 12.8 and 16.1, of 192 13.8 and 16.3, of 256 16.8 and 16.1; 256
+// requests of one token 34 and 43, 512 45.7 and 44.9.
 bool packs(int op, int64_t T, int64_t S) {
   if (op != kLowRankAdd) return op == kLowRankBackward;
   return T > (S >= T / 8 ? 256 : 192);
