@@ -187,8 +187,9 @@ __device__ __forceinline__ void shrink_load_count(const T* p, int64_t ld, int64_
 // Accumulates the steps [s0, s1) of 32 features for the tokens tok..tok+V-1 of
 // each lane and 16 NR ranks from r0.  x is read V tokens wide, eight rows a
 // lane, and turned in registers; the same turn serves a factor stored [K][R].
-// Two steps' rows are in flight where the sums leave room for them (one alone,
-// at three waves a SIMD: 24 us where two take 19, 67 MB of x and dy, 16 ranks).
+// Two steps' rows are in flight where the sums leave room for them, at two waves a
+// SIMD (67 MB of x and dy, 16 ranks: 18.8 us; one step at three waves 19.7, at four,
+// with registers in memory, 22.1).
 template <typename T, int V, int NR, bool TR, bool PACK>
 __device__ __forceinline__ void shrink_steps(const T* x, int64_t ldx, int64_t K, const T* f, int R,
                                              int r0, int64_t tok, int64_t s0, int64_t s1,
