@@ -444,8 +444,10 @@ spops_status spops_delta_spmv(int64_t rows, int64_t cols, const int32_t* enc_off
  * feature-major (features x tokens, unit stride along the tokens).
  *   dtype:   of every matrix (f32, f16 or bf16).  Sums and u are fp32; every
  *            output value is rounded once.
- *   tokens >= 0, requests >= 0, 1 <= adapters <= 65535, 1 <= rank <= 256,
- *   features in 1..2^24.
+ *   tokens in 0..2^30, requests >= 0, 1 <= adapters <= 65535, 1 <= rank <= 256,
+ *   features in 1..2^24; SPOPS_ERR_SHAPE also where a kernel would need more than
+ *   2^31 - 1 workgroups (from tokens x features of 2^39, or adapters x features of
+ *   2^34, on: past any memory).
  *   A:       [adapters][rank][in_features]
  *   B:       [adapters][out_features][rank]
  *   offsets: [requests+1] int32, ascending (equal neighbours: an empty
