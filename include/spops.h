@@ -525,6 +525,74 @@ spops_status spops_clip_grad_norm(const spops_clip_tensor* tensors, int64_t coun
                                   double max_norm, float* norm, void* workspace,
                                   size_t workspace_bytes, void* hip_stream);
 
+/* ------------------------------------ 4-bit microscaled matrices --
+ * A matrix of 4-bit floating-point elements (sign, two bits of exponent, one of
+ * mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6) in blocks of 32 along its rows, each block
+ * with a power of two as its scale (the MXFP4 format of the OCP microscaling
+ * specification 1.0).  With nb = ceil(cols / 32):
+ *   codes:  [rows][16 nb], 16-byte aligned; element 2j of a row is the low half of
+ *           byte j, element 2j + 1 the high half.  Elements past cols are zero.
+ *   scales: [rows][nb]; s stands for 2^(s - 127), 255 makes the block NaN.  (From
+ *           253 on a block's elements may pass the range of f32: infinities.)
+ * rows and cols in 1..2^24. */
+typedef struct spops_mx4 {
+  int64_t rows, cols;
+  const uint8_t* codes;
+  const uint8_t* scales;
+} spops_mx4;
+
+/* w (rows x cols, f32, f16 or bf16) to codes and scales, both written whole.  The
+ * scale of a block is 2^(floor(log2(max |w|)) - 2), at least 2^-127 (1 for a block of
+ * zeros), and an element is w / scale rounded to nearest even, at most 6: values
+ * between 6 and 8 times the scale saturate.  A block that holds an infinity or a NaN
+ * becomes NaN.  Element (r, c) is w[r * row_stride + c * col_stride]; one of the
+ * strides is 1 and the other at least the size along the first, so that activations
+ * of features x tokens are quantised along their features without a copy. */
+spops_status spops_mx4_quantize(const void* w, spops_dtype dtype, int64_t rows, int64_t cols,
+                                int64_t row_stride, int64_t col_stride, uint8_t* codes,
+                                uint8_t* scales, void* hip_stream);
+/* out [rows][cols] (row stride ldo): the values, rounded to dtype (f32 and bf16 hold
+ * all of them). */
+spops_status spops_mx4_dequantize(const spops_mx4* W, void* out, spops_dtype dtype, int64_t ldo,
+                                  void* hip_stream);
+
+/* out = W x for x [cols][tokens], out [rows][tokens]; with `transposed` nonzero
+ * out = W^T x for x [rows][tokens], out [cols][tokens] (the gradient of the input).
+ * x and out have the type dtype and unit stride along the tokens.  Every product is
+ * exact, sums are f32, and each output is rounded once (bits of an f32 x below 2^-133
+ * are left out).  tokens in 0..2^30.  out
+ * overlaps no input.  The workspace is 256-byte aligned (NULL where its size is 0) and
+ * needs no preparation. */
+spops_status spops_mx4_matmul_workspace_size(const spops_mx4* W, int transposed,
+                                             spops_dtype dtype, int64_t tokens, size_t* bytes);
+spops_status spops_mx4_matmul(const spops_mx4* W, int transposed, const void* x,
+                              spops_dtype dtype, int64_t tokens, int64_t ldx, void* out,
+                              int64_t ldo, void* workspace, size_t workspace_bytes,
+                              void* hip_stream);
+/* out [W.rows][X.rows] = W X^T with both in four bits (X: tokens x cols): exact
+ * products, f32 sums, one rounding to dtype. */
+spops_status spops_mx4_matmul4_workspace_size(const spops_mx4* W, int64_t tokens, size_t* bytes);
+spops_status spops_mx4_matmul4(const spops_mx4* W, const spops_mx4* X, void* out,
+                               spops_dtype dtype, int64_t ldo, void* workspace,
+                               size_t workspace_bytes, void* hip_stream);
+
+/* ---------------------------------------------------------- dropout --
+ * out = x * 65536 / (65536 - limit) where an element is kept and 0 where it is not
+ * (whatever x is there), limit = p * 65536 rounded.  Element (r, c) is kept when 16
+ * random bits of its own are at least limit: half c % 8 of the four words of Philox
+ * 4x32 with seven rounds (Salmon et al., 2011) on the counter (c / 8, r, step mod
+ * 2^32, step / 2^32) and the key (seed mod 2^32, seed / 2^32).  The mask is never
+ * stored: the same call on the gradient of out gives that of x.
+ *   x, out: [rows][cols] of dtype, row strides ldx and ldo; out may be x, and overlaps
+ *           it in no other way.  rows and cols in 0..2^31 - 1.
+ *   p in [0, 1] (1: all zeros).
+ *   state:  NULL, or [2] on the device: seed and step are read from there when the
+ *           kernel runs (so that a captured call can draw another mask at each replay)
+ *           and the arguments are not used. */
+spops_status spops_dropout(const void* x, spops_dtype dtype, int64_t rows, int64_t cols,
+                           int64_t ldx, void* out, int64_t ldo, double p, uint64_t seed,
+                           uint64_t step, const uint64_t* state, void* hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,9 +10,12 @@ implementation: calls raise if libspops.so is missing.
 from .adapter import (  # noqa: F401
     LowRankAdapters,
     MaskedAdam,
+    Mx4Linear,
     SparseAdapter,
     SparsePattern,
+    dropout,
     low_rank_linear,
+    mx4_linear,
     sparse_linear,
 )
 from .spops import (  # noqa: F401
@@ -20,6 +23,7 @@ from .spops import (  # noqa: F401
     SpmmPlan,
     DeltaMatrix,
     InvalidCSR,
+    Mx4Matrix,
     SpopsError,
     cg,
     delta_encode,
@@ -35,6 +39,9 @@ from .spops import (  # noqa: F401
     low_rank_backward,
     low_rank_project,
     masked_adam,
+    mx4_dequantize,
+    mx4_matmul,
+    mx4_quantize,
     option,
     permute_values,
     sddmm,
@@ -51,4 +58,5 @@ __all__ = ["spmm", "sddmm", "csr_add", "csr_transpose", "sort_rows_by_nnz", "Spm
            "masked_adam", "MaskedAdam", "DeltaMatrix", "delta_encode", "delta_spmv",
            "option", "set_option", "validate_csr", "InvalidCSR", "csr_transpose_permutation",
            "permute_values", "low_rank_add", "low_rank_project", "low_rank_backward",
-           "low_rank_linear", "LowRankAdapters", "clip_grad_norm"]
+           "low_rank_linear", "LowRankAdapters", "clip_grad_norm", "Mx4Matrix", "Mx4Linear",
+           "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_linear", "dropout"]

@@ -20,14 +20,14 @@ is computed by the library's kernels (it raises if libspops.so is missing).
 """
 from __future__ import annotations
 
-from typing import Optional
+from typing import Optional, Union
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from .spops import (SddmmPlan, SpmmPlan, csr_add, csr_transpose_permutation, low_rank_add,
-                    low_rank_backward, low_rank_project, masked_adam, permute_values, sddmm,
-                    sort_rows_by_nnz, spmm)
+from .spops import (Mx4Matrix, SddmmPlan, SpmmPlan, _marshal, csr_add, csr_transpose_permutation,
+                    low_rank_add, low_rank_backward, low_rank_project, masked_adam, mx4_matmul,
+                    mx4_quantize, permute_values, sddmm, sort_rows_by_nnz, spmm)
 
 
 class SparsePattern:
@@ -112,6 +112,83 @@ class SparseAdapter(torch.nn.Module):
         return csr_add(self.values.detach(), P.ro, P.ri, P.ci, W)
 
 
+class _Mx4LinearFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, xt, codes, scales, cols, transposed):
+        ctx.save_for_backward(codes, scales)
+        ctx.cols, ctx.transposed = cols, transposed
+        return mx4_matmul(Mx4Matrix(codes, scales, cols), xt, transposed)
+
+    @staticmethod
+    def backward(ctx, dyt):
+        codes, scales = ctx.saved_tensors
+        return (_Mx4LinearFn.apply(dyt.contiguous(), codes, scales, ctx.cols, not ctx.transposed),
+                None, None, None, None)
+
+
+def mx4_linear(W: Mx4Matrix, xt: torch.Tensor) -> torch.Tensor:
+    """W · X^T for a frozen W in four bits; differentiable in X^T (any number of
+    times: the gradient is mx4_matmul with W transposed)."""
+    return _Mx4LinearFn.apply(xt, W.codes, W.scales, W.cols, False)
+
+
+class Mx4Linear(torch.nn.Module):
+    """A frozen layer of out_features x in_features in 4-bit microscaled form:
+    forward(X^T) = W · X^T in the dtype of X^T, differentiable in X^T.  `weight` is a
+    matrix to quantise or an Mx4Matrix.  Adapters train on top of it:
+    adapters(base(xt), xt, offsets, adapter)."""
+
+    def __init__(self, weight: Union[torch.Tensor, Mx4Matrix]):
+        super().__init__()
+        W = weight if isinstance(weight, Mx4Matrix) else mx4_quantize(weight.detach())
+        self.cols = W.cols
+        self.register_buffer("codes", W.codes)
+        self.register_buffer("scales", W.scales)
+
+    @property
+    def weight(self) -> Mx4Matrix:
+        return Mx4Matrix(self.codes, self.scales, self.cols)
+
+    def forward(self, xt: torch.Tensor) -> torch.Tensor:
+        return _Mx4LinearFn.apply(xt, self.codes, self.scales, self.cols, False)
+
+
+class _DropoutFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, seed, step):
+        ctx.p, ctx.step = p, step
+        ctx.seed = seed
+        if isinstance(seed, torch.Tensor):
+            ctx.save_for_backward(seed)
+            ctx.seed = None
+        return _marshal().dropout(x, p, seed, step, None)
+
+    @staticmethod
+    def backward(ctx, dy):
+        seed = ctx.saved_tensors[0] if ctx.seed is None else ctx.seed
+        return _DropoutFn.apply(dy.contiguous(), ctx.p, seed, ctx.step), None, None, None
+
+
+def dropout(x: torch.Tensor, p: float, seed: Union[int, torch.Tensor], step: int = 0,
+            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x with each element set to zero with probability p and the others scaled up to
+    keep the mean; the mask is a function of the element's place, seed and step alone
+    and is never stored.
+
+    The place is (row, column): of a matrix, or of a contiguous tensor whose last
+    dimension are the columns.  An element is dropped when 16 random bits of it are
+    below limit = round(65536 p), and kept ones are scaled by 65536 / (65536 - limit).
+    `seed` is a number or an int64 vector of seed and step on the device, which is read
+    when the kernel runs (a captured call then takes what it holds at each replay).
+    Differentiable in x (the gradient is the same call on dy; a vector `seed` must not
+    change before it), unless `out` is given, which may be x."""
+    if out is not None or not (x.requires_grad and torch.is_grad_enabled()):
+        if out is not None and torch.is_grad_enabled() and (x.requires_grad or out.requires_grad):
+            raise ValueError("dropout into out has no gradient; detach x")
+        return _marshal().dropout(x, p, seed, step, out)
+    return _DropoutFn.apply(x, p, seed, step)
+
+
 class _LowRankLinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, yt, xt, A, B, offsets, adapter, scale, ranks):
@@ -149,16 +226,25 @@ class LowRankAdapters(torch.nn.Module):
       forward(yt, xt, offsets, adapter)   yt + the requests' adapters, for
                                           training and prompts
       project(W, xt, offsets, adapter)    W xt + the same in one pass over W,
-                                          for decode steps (no gradient)
+                                          for decode steps (no gradient, no
+                                          dropout)
 
-    yt may come from any layer on xt, a dense product or a SparseAdapter.  scale
-    and ranks (one value per adapter, of any device and type) are kept as float32
-    and int32 buffers, also where the module is cast."""
+    yt may come from any layer on xt, a dense product, a SparseAdapter or an Mx4Linear;
+    W may be an Mx4Matrix.  scale and ranks (one value per adapter, of any device and
+    type) are kept as float32 and int32 buffers, also where the module is cast.
+
+    With dropout = p, forward in training drops elements of xt on the adapters' side
+    (not in yt) with probability p.  The masks follow from `dropout_state`, an int64
+    buffer of a seed and a step that each such call advances on the device; seed
+    defaults to a number of torch's generator."""
 
     def __init__(self, adapters: int, rank: int, in_features: int, out_features: int,
                  scale: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None,
-                 dtype: torch.dtype = torch.float32, device="cuda"):
+                 dtype: torch.dtype = torch.float32, device="cuda", dropout: float = 0.0,
+                 seed: Optional[int] = None):
         super().__init__()
+        if not 0.0 <= dropout <= 1.0:
+            raise ValueError("dropout must be between 0 and 1")
         A = torch.randn(adapters, rank, in_features, device=device) * in_features ** -0.5
         self.A = torch.nn.Parameter(A.to(dtype))
         self.B = torch.nn.Parameter(torch.zeros(adapters, out_features, rank, dtype=dtype,
@@ -167,6 +253,12 @@ class LowRankAdapters(torch.nn.Module):
         self.register_buffer("scale", scale if scale is None else
                              scale.to(device, torch.float32))
         self.register_buffer("ranks", ranks if ranks is None else ranks.to(device, torch.int32))
+        self.dropout = dropout
+        if dropout > 0.0:
+            if seed is None:
+                seed = int(torch.randint(1 << 62, (), dtype=torch.int64))
+            self.register_buffer("dropout_state",
+                                 torch.tensor([seed, 0], dtype=torch.int64, device=device))
 
     def _apply(self, fn, *args, **kwargs):
         """Moves and casts of the module: scale moves, but stays float32 with the
@@ -179,11 +271,20 @@ class LowRankAdapters(torch.nn.Module):
 
     def forward(self, yt: torch.Tensor, xt: torch.Tensor, offsets: torch.Tensor,
                 adapter: torch.Tensor) -> torch.Tensor:
+        if self.training and self.dropout > 0.0:
+            # the backward pass draws the mask again from a copy of the state
+            state = self.dropout_state.clone()
+            self.dropout_state[1].add_(1)
+            xt = dropout(xt, self.dropout, state)
         return low_rank_linear(yt, xt, self.A, self.B, offsets, adapter, self.scale, self.ranks)
 
     @torch.no_grad()
-    def project(self, W: torch.Tensor, xt: torch.Tensor, offsets: torch.Tensor,
+    def project(self, W: Union[torch.Tensor, Mx4Matrix], xt: torch.Tensor, offsets: torch.Tensor,
                 adapter: torch.Tensor) -> torch.Tensor:
+        if isinstance(W, Mx4Matrix):
+            yt = mx4_matmul(W, xt)
+            return low_rank_add(yt, xt, self.A, self.B, offsets, adapter, self.scale, self.ranks,
+                                out=yt)
         return low_rank_project(W, xt, self.A, self.B, offsets, adapter, self.scale, self.ranks)
 
 

@@ -1075,4 +1075,147 @@ spops_status spops_clip_grad_norm(const spops_clip_tensor* tensors, int64_t coun
                               as_stream(hip_stream)));
 }
 
+// -------------------------------------- 4-bit microscaled matrices --
+
+namespace {
+
+constexpr int64_t kMx4MaxSize = (int64_t)1 << 24;
+constexpr int64_t kMx4MaxTokens = (int64_t)1 << 30;
+
+bool mx4_size(int64_t rows, int64_t cols) {
+  return rows >= 1 && rows <= kMx4MaxSize && cols >= 1 && cols <= kMx4MaxSize;
+}
+spops_status check_mx4(const spops_mx4* W) {
+  if (!W) return SPOPS_ERR_NULL;
+  if (!mx4_size(W->rows, W->cols)) return SPOPS_ERR_SHAPE;
+  if (!W->codes || !W->scales) return SPOPS_ERR_NULL;
+  if ((uintptr_t)W->codes & 15) return SPOPS_ERR_SHAPE;
+  return SPOPS_OK;
+}
+Mx4 mx4_of(const spops_mx4* W) { return {W->rows, W->cols, W->codes, W->scales}; }
+// Tiles of an output are counted in 32 bits, and so are their threads (of any memory
+// the outputs of the sizes that are refused take the whole).
+bool mx4_output(int64_t rows, int64_t tokens) {
+  return ((rows + 127) / 128) * ((tokens + 127) / 128) <= (1 << 23);
+}
+spops_status workspace_ok(const void* ws, size_t have, size_t want) {
+  if (want > 0 && (!ws || have < want || ((uintptr_t)ws & 255))) return SPOPS_ERR_WORKSPACE;
+  return SPOPS_OK;
+}
+
+}  // namespace
+
+spops_status spops_mx4_quantize(const void* w, spops_dtype dtype, int64_t rows, int64_t cols,
+                                int64_t row_stride, int64_t col_stride, uint8_t* codes,
+                                uint8_t* scales, void* hip_stream) {
+  if (!dtype_ok(dtype)) return SPOPS_ERR_DTYPE;
+  if (!mx4_size(rows, cols)) return SPOPS_ERR_SHAPE;
+  const bool along_rows = col_stride == 1 && (rows == 1 || row_stride >= cols);
+  const bool along_cols = row_stride == 1 && (cols == 1 || col_stride >= rows);
+  if (!along_rows && !along_cols) return SPOPS_ERR_SHAPE;
+  if (!w || !codes || !scales) return SPOPS_ERR_NULL;
+  if ((uintptr_t)codes & 15) return SPOPS_ERR_SHAPE;
+  return from_hip(launch_mx4_quantize(w, dtype, rows, cols, along_rows ? row_stride : 1,
+                                      along_rows ? 1 : col_stride, codes, scales,
+                                      as_stream(hip_stream)));
+}
+
+spops_status spops_mx4_dequantize(const spops_mx4* W, void* out, spops_dtype dtype, int64_t ldo,
+                                  void* hip_stream) {
+  if (!dtype_ok(dtype)) return SPOPS_ERR_DTYPE;
+  const spops_status st = check_mx4(W);
+  if (st != SPOPS_OK) return st;
+  if (ldo < W->cols) return SPOPS_ERR_SHAPE;
+  if (!out) return SPOPS_ERR_NULL;
+  return from_hip(launch_mx4_dequantize(mx4_of(W), out, dtype, ldo, as_stream(hip_stream)));
+}
+
+spops_status spops_mx4_matmul_workspace_size(const spops_mx4* W, int transposed,
+                                             spops_dtype dtype, int64_t tokens, size_t* bytes) {
+  if (!dtype_ok(dtype)) return SPOPS_ERR_DTYPE;
+  if (!W || !bytes) return SPOPS_ERR_NULL;
+  if (!mx4_size(W->rows, W->cols) || tokens < 0 || tokens > kMx4MaxTokens ||
+      !mx4_output(transposed ? W->cols : W->rows, tokens))
+    return SPOPS_ERR_SHAPE;
+  *bytes = tokens == 0 ? 0 : mx4_matmul_bytes(mx4_of(W), transposed != 0, dtype, tokens);
+  return SPOPS_OK;
+}
+
+spops_status spops_mx4_matmul(const spops_mx4* W, int transposed, const void* x,
+                              spops_dtype dtype, int64_t tokens, int64_t ldx, void* out,
+                              int64_t ldo, void* workspace, size_t workspace_bytes,
+                              void* hip_stream) {
+  if (!dtype_ok(dtype)) return SPOPS_ERR_DTYPE;
+  spops_status st = check_mx4(W);
+  if (st != SPOPS_OK) return st;
+  const Mx4 w = mx4_of(W);
+  if (tokens < 0 || tokens > kMx4MaxTokens || ldx < tokens || ldo < tokens ||
+      !mx4_output(transposed ? w.cols : w.rows, tokens))
+    return SPOPS_ERR_SHAPE;
+  if (tokens == 0) return SPOPS_OK;
+  if (!x || !out) return SPOPS_ERR_NULL;
+  st = workspace_ok(workspace, workspace_bytes, mx4_matmul_bytes(w, transposed != 0, dtype, tokens));
+  if (st != SPOPS_OK) return st;
+  Mx4MatmulArgs a{};
+  a.W = w;
+  a.x = x;
+  a.out = out;
+  a.T = tokens;
+  a.ldx = ldx;
+  a.ldo = ldo;
+  a.part = (float*)workspace;
+  return from_hip(launch_mx4_matmul(a, transposed != 0, dtype, as_stream(hip_stream)));
+}
+
+spops_status spops_mx4_matmul4_workspace_size(const spops_mx4* W, int64_t tokens, size_t* bytes) {
+  if (!W || !bytes) return SPOPS_ERR_NULL;
+  if (!mx4_size(W->rows, W->cols) || tokens < 0 || tokens > kMx4MaxSize ||
+      !mx4_output(W->rows, tokens))
+    return SPOPS_ERR_SHAPE;
+  *bytes = tokens == 0 ? 0 : mx4_matmul4_bytes(mx4_of(W), tokens);
+  return SPOPS_OK;
+}
+
+spops_status spops_mx4_matmul4(const spops_mx4* W, const spops_mx4* X, void* out,
+                               spops_dtype dtype, int64_t ldo, void* workspace,
+                               size_t workspace_bytes, void* hip_stream) {
+  if (!dtype_ok(dtype)) return SPOPS_ERR_DTYPE;
+  spops_status st = check_mx4(W);
+  if (st == SPOPS_OK) st = check_mx4(X);
+  if (st != SPOPS_OK) return st;
+  if (X->cols != W->cols || ldo < X->rows || !mx4_output(W->rows, X->rows)) return SPOPS_ERR_SHAPE;
+  if (!out) return SPOPS_ERR_NULL;
+  const Mx4 w = mx4_of(W);
+  st = workspace_ok(workspace, workspace_bytes, mx4_matmul4_bytes(w, X->rows));
+  if (st != SPOPS_OK) return st;
+  return from_hip(launch_mx4_matmul4(w, mx4_of(X), out, dtype, ldo, workspace,
+                                     as_stream(hip_stream)));
+}
+
+// ------------------------------------------------------------- dropout --
+
+spops_status spops_dropout(const void* x, spops_dtype dtype, int64_t rows, int64_t cols,
+                           int64_t ldx, void* out, int64_t ldo, double p, uint64_t seed,
+                           uint64_t step, const uint64_t* state, void* hip_stream) {
+  if (!dtype_ok(dtype)) return SPOPS_ERR_DTYPE;
+  if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > INT32_MAX || ldx < cols || ldo < cols)
+    return SPOPS_ERR_SHAPE;
+  if (!(p >= 0.0 && p <= 1.0)) return SPOPS_ERR_ARGUMENT;
+  if (rows == 0 || cols == 0) return SPOPS_OK;
+  if (!x || !out) return SPOPS_ERR_NULL;
+  DropoutArgs a{};
+  a.x = x;
+  a.out = out;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = ldx;
+  a.ldo = ldo;
+  a.state = state;
+  a.seed = seed;
+  a.step = step;
+  a.limit = (uint32_t)(p * 65536.0 + 0.5);
+  a.scale = a.limit < 65536u ? (float)(65536.0 / (65536.0 - a.limit)) : 0.f;
+  return from_hip(launch_dropout(a, dtype, as_stream(hip_stream)));
+}
+
 }  // extern "C"

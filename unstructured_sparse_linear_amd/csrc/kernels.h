@@ -452,4 +452,43 @@ size_t clip_workspace_bytes(int64_t count);
 hipError_t launch_clip(const ClipTensor* t, int64_t count, double max_norm, float* norm, void* ws,
                        hipStream_t s);
 
+// ------------------------------------- 4-bit microscaled matrices --
+struct Mx4 {
+  int64_t rows, cols;
+  const uint8_t* codes;   // [rows][16 ceil(cols / 32)]
+  const uint8_t* scales;  // [rows][ceil(cols / 32)]
+};
+hipError_t launch_mx4_quantize(const void* w, int dtype, int64_t rows, int64_t cols, int64_t rs,
+                               int64_t cs, uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_mx4_dequantize(const Mx4& W, void* out, int dtype, int64_t ldo, hipStream_t s);
+
+struct Mx4MatmulArgs {
+  Mx4 W;
+  const void* x;           // [W.cols][T], transposed [W.rows][T]
+  void* out;               // [W.rows][T], transposed [W.cols][T]
+  int64_t T, ldx, ldo;
+  float* part;             // sums of the pieces of the inner size, [pieces][rows out][T]
+  int32_t pieces, steps;   // pieces, and steps of 64 in each
+};
+// Workspace bytes of a product.
+size_t mx4_matmul_bytes(const Mx4& W, int transposed, int dtype, int64_t T);
+hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, int transposed, int dtype, hipStream_t s);
+// out = W X^T for X of tokens x W.cols, both in four bits.
+size_t mx4_matmul4_bytes(const Mx4& W, int64_t T);
+hipError_t launch_mx4_matmul4(const Mx4& W, const Mx4& X, void* out, int dtype, int64_t ldo,
+                              void* ws, hipStream_t s);
+
+// ------------------------------------------------------------- dropout --
+struct DropoutArgs {
+  const void* x;
+  void* out;
+  int64_t rows, cols, ldx, ldo;
+  int64_t row0;            // the launch's first row
+  const uint64_t* state;   // seed and step on the device, or null
+  uint64_t seed, step;
+  uint32_t limit;          // of 65536 elements, those that are dropped
+  float scale;
+};
+hipError_t launch_dropout(DropoutArgs a, int dtype, hipStream_t s);
+
 }  // namespace spops

@@ -1,8 +1,8 @@
 // marshal.cpp -- the part of the Python binding whose calls are too short for
-// interpreted marshalling: the low-rank adapters (a decode step's call takes a
-// few microseconds on the GPU) and gradient clipping (hundreds of tensors a
-// call).  Checks the tensors, allocates outputs and workspace on the current
-// stream and calls libspops; it computes nothing.
+// interpreted marshalling: the low-rank adapters and the 4-bit matrices (a decode
+// step's call takes a few microseconds on the GPU), dropout and gradient clipping
+// (hundreds of tensors a call).  Checks the tensors, allocates outputs and workspace
+// on the current stream and calls libspops; it computes nothing.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -353,11 +353,265 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// -------------------------------------- 4-bit microscaled matrices --
+
+int64_t mx4_blocks(int64_t cols) { return (cols + 31) / 32; }
+
+int64_t whole(PyObject* o) {
+  const int64_t v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw PythonError{};
+  return v;
+}
+
+// codes, scales and the number of columns of a matrix.
+struct Mx4Ref {
+  const at::Tensor &codes, &scales;
+  spops_mx4 d{};
+  explicit Mx4Ref(PyObject* const* args) : codes(tensor(args[0], "codes")),
+                                           scales(tensor(args[1], "scales")) {
+    d.cols = whole(args[2]);
+    need(codes.scalar_type() == at::kByte && codes.dim() == 2, "codes", "must be a matrix of uint8");
+    need(scales.scalar_type() == at::kByte && scales.dim() == 2, "scales",
+         "must be a matrix of uint8");
+    contiguous(codes, "codes");
+    contiguous(scales, "scales");
+    d.rows = codes.size(0);
+    const int64_t nb = mx4_blocks(d.cols);
+    need(d.cols >= 1 && codes.size(1) == 16 * nb, "codes", "must be rows x 16 ceil(cols / 32)");
+    need(scales.size(0) == d.rows && scales.size(1) == nb, "scales",
+         "must be rows x ceil(cols / 32)");
+    need(((uintptr_t)codes.data_ptr() & 15) == 0, "codes", "must be aligned to 16 bytes");
+    d.codes = (const uint8_t*)codes.data_ptr();
+    d.scales = (const uint8_t*)scales.data_ptr();
+  }
+  void device(c10::Device dev) const {
+    same_device(codes, "codes", dev);
+    same_device(scales, "scales", dev);
+  }
+};
+
+// `out` as given (its dtype, shape and place checked) or a new matrix.
+struct Output {
+  at::Tensor t;
+  int64_t ld;
+  bool into;
+  Output(PyObject* o, at::ScalarType type, int64_t rows, int64_t cols,
+         const at::TensorOptions& options, const char* shape)
+      : into(given(o)) {
+    if (into) {
+      t = tensor(o, "out");
+      need(t.scalar_type() == type, "out", "must have the dtype of the result");
+      leading(t, "out");
+      need(t.size(0) == rows && t.size(1) == cols, "out", shape);
+      same_device(t, "out", options.device());
+    } else {
+      t = at::empty({rows, cols}, options.dtype(type));
+    }
+    ld = leading(t, "out");
+  }
+  PyObject* result(PyObject* o) {
+    if (!into) return THPVariable_Wrap(t);
+    written(t);
+    Py_INCREF(o);
+    return o;
+  }
+};
+
+at::ScalarType scalar_type(int64_t dtype) {
+  need(dtype >= SPOPS_F32 && dtype <= SPOPS_BF16, "dtype", "must be float32, float16 or bfloat16");
+  return dtype == SPOPS_F32 ? at::kFloat : dtype == SPOPS_F16 ? at::kHalf : at::kBFloat16;
+}
+
+at::Tensor bytes_of(size_t n, const at::TensorOptions& options) {
+  return n ? at::empty({(int64_t)n}, options.dtype(at::kByte)) : at::Tensor();
+}
+
+PyObject* mx4_quantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!count_args(n, 1)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& w = tensor(args[0], "w");
+    const spops_dtype dt = dtype_of(w, "w");
+    need(w.layout() == at::kStrided, "w", "must be a dense tensor");
+    need(w.dim() == 2, "w", "must be a matrix");
+    const int64_t rows = w.size(0), cols = w.size(1);
+    need(rows >= 1 && cols >= 1, "w", "must not be empty");
+    // a stride along a size of one says nothing
+    int64_t rs = rows == 1 ? cols : w.stride(0), cs = cols == 1 ? 1 : w.stride(1);
+    if (!(cs == 1 && rs >= cols)) {
+      rs = rows == 1 ? 1 : rs;
+      cs = cols == 1 ? rows : cs;
+      need(rs == 1 && cs >= rows, "w",
+           "must have unit stride along its rows or its columns and no overlaps");
+    }
+    const c10::Device dev = w.device();
+    same_device(w, "w", dev);
+    const c10::DeviceGuard guard(dev);
+    const at::TensorOptions options = w.options().dtype(at::kByte);
+    const int64_t nb = mx4_blocks(cols);
+    const at::Tensor codes = at::empty({rows, 16 * nb}, options);
+    const at::Tensor scales = at::empty({rows, nb}, options);
+    status("spops_mx4_quantize",
+           spops_mx4_quantize(w.data_ptr(), dt, rows, cols, rs, cs, (uint8_t*)codes.data_ptr(),
+                              (uint8_t*)scales.data_ptr(), stream_of(dev)));
+    return Py_BuildValue("(NN)", THPVariable_Wrap(codes), THPVariable_Wrap(scales));
+  });
+}
+
+// codes, scales, cols, dtype, out
+PyObject* mx4_dequantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!count_args(n, 5)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Mx4Ref W(args);
+    const int64_t dt = whole(args[3]);
+    const at::ScalarType type = scalar_type(dt);
+    const c10::Device dev = W.codes.device();
+    W.device(dev);
+    const c10::DeviceGuard guard(dev);
+    Output out(args[4], type, W.d.rows, W.d.cols, W.codes.options(), "must be rows x cols");
+    status("spops_mx4_dequantize", spops_mx4_dequantize(&W.d, out.t.data_ptr(), (spops_dtype)dt,
+                                                        out.ld, stream_of(dev)));
+    return out.result(args[4]);
+  });
+}
+
+// codes, scales, cols, x, transposed, out
+PyObject* mx4_matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!count_args(n, 6)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Mx4Ref W(args);
+    const at::Tensor& x = tensor(args[3], "xt");
+    const int transposed = whole(args[4]) != 0;
+    const spops_dtype dt = dtype_of(x, "xt");
+    const int64_t ldx = leading(x, "xt");
+    const int64_t inner = transposed ? W.d.rows : W.d.cols;
+    const int64_t rows = transposed ? W.d.cols : W.d.rows, tokens = x.size(1);
+    need(x.size(0) == inner, "xt",
+         transposed ? "must be W's rows x tokens" : "must be W's columns x tokens");
+    const c10::Device dev = x.device();
+    same_device(x, "xt", dev);
+    W.device(dev);
+    const c10::DeviceGuard guard(dev);
+    Output out(args[5], x.scalar_type(), rows, tokens, x.options(), "must be features x tokens");
+    need(!out.into || !spans_meet(out.t, out.ld, x, ldx), "out", "must not overlap xt");
+    size_t bytes = 0;
+    status("spops_mx4_matmul_workspace_size",
+           spops_mx4_matmul_workspace_size(&W.d, transposed, dt, tokens, &bytes));
+    const at::Tensor ws = bytes_of(bytes, x.options());
+    status("spops_mx4_matmul",
+           spops_mx4_matmul(&W.d, transposed, x.data_ptr(), dt, tokens, ldx, out.t.data_ptr(),
+                            out.ld, ws.defined() ? ws.data_ptr() : nullptr, bytes, stream_of(dev)));
+    return out.result(args[5]);
+  });
+}
+
+// codes, scales, cols of W; codes, scales, cols of X; dtype, out
+PyObject* mx4_matmul4(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!count_args(n, 8)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Mx4Ref W(args), X(args + 3);
+    const int64_t dt = whole(args[6]);
+    const at::ScalarType type = scalar_type(dt);
+    need(X.d.cols == W.d.cols, "xt", "must have W's columns");
+    const c10::Device dev = W.codes.device();
+    W.device(dev);
+    X.device(dev);
+    const c10::DeviceGuard guard(dev);
+    Output out(args[7], type, W.d.rows, X.d.rows, W.codes.options(), "must be features x tokens");
+    size_t bytes = 0;
+    status("spops_mx4_matmul4_workspace_size",
+           spops_mx4_matmul4_workspace_size(&W.d, X.d.rows, &bytes));
+    const at::Tensor ws = bytes_of(bytes, W.codes.options());
+    status("spops_mx4_matmul4",
+           spops_mx4_matmul4(&W.d, &X.d, out.t.data_ptr(), (spops_dtype)dt, out.ld,
+                             ws.defined() ? ws.data_ptr() : nullptr, bytes, stream_of(dev)));
+    return out.result(args[7]);
+  });
+}
+
+// ------------------------------------------------------------- dropout --
+
+// Rows of unit stride of a tensor of any shape: a matrix with its row stride, others
+// contiguous.
+int64_t rows_of(const at::Tensor& t, const char* name, int64_t& rows, int64_t& cols) {
+  need(t.layout() == at::kStrided, name, "must be a dense tensor");
+  if (t.dim() == 2) {
+    rows = t.size(0);
+    cols = t.size(1);
+    return leading(t, name);
+  }
+  need(t.is_contiguous(), name, "must be contiguous or a matrix");
+  cols = t.dim() ? t.size(-1) : 1;
+  rows = t.dim() == 0 ? 1 : cols ? t.numel() / cols : 0;
+  return cols ? cols : 1;
+}
+
+// x, p, seed or state, step, out
+PyObject* dropout(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!count_args(n, 5)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const at::Tensor& x = tensor(args[0], "x");
+    const spops_dtype dt = dtype_of(x, "x");
+    int64_t rows, cols, out_rows, out_cols;
+    const int64_t ldx = rows_of(x, "x", rows, cols);
+    const double p = PyFloat_AsDouble(args[1]);
+    if (p == -1.0 && PyErr_Occurred()) throw PythonError{};
+    need(p >= 0.0 && p <= 1.0, "p", "must be between 0 and 1");
+    const bool on_device = THPVariable_Check(args[2]);
+    uint64_t seed = 0, step = 0;
+    const uint64_t* state = nullptr;
+    if (on_device) {
+      const at::Tensor& t = THPVariable_Unpack(args[2]);
+      need(t.scalar_type() == at::kLong && t.dim() == 1 && t.numel() == 2, "seed",
+           "must be a number or an int64 vector of seed and step");
+      contiguous(t, "seed");
+      state = (const uint64_t*)t.data_ptr();
+    } else {
+      seed = PyLong_AsUnsignedLongLongMask(args[2]);
+      if (PyErr_Occurred()) throw PythonError{};
+      step = PyLong_AsUnsignedLongLongMask(args[3]);
+      if (PyErr_Occurred()) throw PythonError{};
+    }
+    const bool into = given(args[4]);
+    if (into) {
+      const at::Tensor& o = tensor(args[4], "out");
+      need(o.scalar_type() == x.scalar_type() && o.sizes() == x.sizes(), "out",
+           "must have x's dtype and shape");
+    }
+    const c10::Device dev = x.device();
+    same_device(x, "x", dev);
+    if (on_device) same_device(THPVariable_Unpack(args[2]), "seed", dev);
+    if (into) same_device(THPVariable_Unpack(args[4]), "out", dev);
+    const c10::DeviceGuard guard(dev);
+    const at::Tensor out = into ? THPVariable_Unpack(args[4]) : at::empty(x.sizes(), x.options());
+    const int64_t ldo = rows_of(out, "out", out_rows, out_cols);
+    if (into && x.numel() && !(out.data_ptr() == x.data_ptr() && (rows <= 1 || ldo == ldx))) {
+      const auto end = [&](const at::Tensor& t, int64_t ld) {
+        return (const char*)t.data_ptr() + ((rows - 1) * ld + cols) * t.element_size();
+      };
+      need((const char*)out.data_ptr() >= end(x, ldx) || (const char*)x.data_ptr() >= end(out, ldo),
+           "out", "must be x or not overlap it");
+    }
+    status("spops_dropout", spops_dropout(x.data_ptr(), dt, rows, cols, ldx, out.data_ptr(), ldo, p,
+                                          seed, step, state, stream_of(dev)));
+    if (into) {
+      written(out);
+      Py_INCREF(args[4]);
+      return args[4];
+    }
+    return THPVariable_Wrap(out);
+  });
+}
+
 PyMethodDef methods[] = {
     {"low_rank_add", (PyCFunction)(void*)low_rank_add, METH_FASTCALL, nullptr},
     {"low_rank_project", (PyCFunction)(void*)low_rank_project, METH_FASTCALL, nullptr},
     {"low_rank_backward", (PyCFunction)(void*)low_rank_backward, METH_FASTCALL, nullptr},
     {"clip_grad_norm", (PyCFunction)(void*)clip_grad_norm, METH_FASTCALL, nullptr},
+    {"mx4_quantize", (PyCFunction)(void*)mx4_quantize, METH_FASTCALL, nullptr},
+    {"mx4_dequantize", (PyCFunction)(void*)mx4_dequantize, METH_FASTCALL, nullptr},
+    {"mx4_matmul", (PyCFunction)(void*)mx4_matmul, METH_FASTCALL, nullptr},
+    {"mx4_matmul4", (PyCFunction)(void*)mx4_matmul4, METH_FASTCALL, nullptr},
+    {"dropout", (PyCFunction)(void*)dropout, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,117 @@
+// mx4.h -- device helpers of the 4-bit microscaled matrices (mx4.hip,
+// mx4_matmul.hip, mx4_mma.hip).
+//
+// A row holds blocks of 32 elements: 16 bytes of codes (element 2j is the low half
+// of byte j; sign, two bits of exponent, one of mantissa) and one scale byte s that
+// stands for 2^(s - 127), or NaN at 255.  gfx950 converts pairs of elements with
+// the scale applied in one instruction, exactly as far as the target type holds the
+// value: bf16 and f32 hold all of them (scales from 253 on pass their range), f16
+// those of the scales 104 to 140.  The conversions take the scale as the exponent
+// field of an f32, where zero stands for 2^-127 and 255 for NaN.
+#pragma once
+
+#include "common.h"
+
+namespace spops {
+
+constexpr int kMx4Block = 32;
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ float mx4_scale(uint32_t code) { return __uint_as_float(code << 23); }
+
+// Elements 2 S and 2 S + 1 of a word of eight, as a pair of 16 bits.
+template <int S>
+__device__ __forceinline__ uint32_t mx4_pair(uint32_t w, float scale, bf16_t*) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, S));
+}
+template <int S>
+__device__ __forceinline__ uint32_t mx4_pair(uint32_t w, float scale, _Float16*) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, S));
+}
+template <int S>
+__device__ __forceinline__ f32x2 mx4_pair_f32(uint32_t w, float scale) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, scale, S);
+}
+
+// A word of eight elements as eight values of 16 bits.
+template <typename T>
+__device__ __forceinline__ uint4 mx4_eight(uint32_t w, float scale) {
+  T* const t = nullptr;
+  return make_uint4(mx4_pair<0>(w, scale, t), mx4_pair<1>(w, scale, t), mx4_pair<2>(w, scale, t),
+                    mx4_pair<3>(w, scale, t));
+}
+
+// The scale byte of a block whose largest magnitude has the f32 bits `top`: the
+// largest power of two with top below 8 times it, so that the largest element (6)
+// is reached and values between 6 and 8 times it saturate.  A block of zeros has
+// scale 1, one that holds an infinity or a NaN has 255.
+__device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t top) {
+  if (top >= 0x7f800000u) return 255u;
+  if (top == 0u) return 127u;
+  const int e = (int)(top >> 23) - 2;
+  return e > 0 ? (uint32_t)e : 0u;
+}
+
+// Eight values to eight codes (round to nearest even, saturating).
+__device__ __forceinline__ uint32_t mx4_encode(const float (&v)[8], float scale) {
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], scale, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], scale, 3);
+  return w;
+}
+
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Workgroup index -> logical index, so that neighbours run on one XCD (workgroup b is
+// on XCD b mod 8).
+__device__ __forceinline__ uint32_t xcd_index(uint32_t b, uint32_t n) {
+  const uint32_t q = b % 8, each = n / 8, more = n % 8;
+  return q * each + min(q, more) + b / 8;
+}
+
+// A 32 x 32 result of v_mfma_f32_32x32x* whose rows are tokens and whose columns are
+// rows of W: a lane holds row r0 + lane % 32 and runs of four tokens.  To `out`
+// ([M][tokens], ldo), or, where the inner size is cut, to piece `piece` of `part`.
+template <typename T>
+__device__ __forceinline__ void mx4_write(const f32x16& acc, int64_t r0, int64_t t0, int64_t M,
+                                          int64_t tokens, void* out, int64_t ldo, float* part,
+                                          uint32_t piece) {
+  const int lane = lane_id();
+  const int64_t r = r0 + lane % 32;
+  if (r >= M) return;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int64_t t = t0 + 8 * g + 4 * (lane / 32);
+    if (part) {
+      float* const p = part + ((int64_t)piece * M + r) * tokens + t;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t + i < tokens) p[i] = acc[4 * g + i];
+    } else {
+      T* const p = (T*)out + r * ldo + t;
+      T v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = from_f32<T>(acc[4 * g + i]);
+      if (t + 4 <= tokens) {
+        __builtin_memcpy(p, v, sizeof(v));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (t + i < tokens) p[i] = v[i];
+      }
+    }
+  }
+}
+
+// out = the sums of the pieces, added in order (mx4.hip).
+hipError_t launch_mx4_sum(const float* part, int pieces, int64_t M, int64_t tokens, void* out,
+                          int dtype, int64_t ldo, hipStream_t s);
+
+}  // namespace spops

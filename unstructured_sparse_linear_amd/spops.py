@@ -1,5 +1,5 @@
-"""Python binding of libspops (ctypes; the low-rank adapter and clipping calls go
-through the compiled _marshal.so).  Argument marshalling only: every step
+"""Python binding of libspops (ctypes; the low-rank adapter, 4-bit matrix, dropout and
+clipping calls go through the compiled _marshal.so).  Argument marshalling only: every step
 of every operation runs in the HIP kernels behind the C ABI in
 include/spops.h; PyTorch provides device memory and the current stream.
 
@@ -61,6 +61,12 @@ class LowRankDesc(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
                 ("offsets", ctypes.c_void_p), ("adapter", ctypes.c_void_p),
                 ("ranks", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class Mx4Desc(ctypes.Structure):
+    """spops_mx4 of include/spops.h."""
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
 
 
 class ClipTensor(ctypes.Structure):
@@ -129,6 +135,14 @@ def lib() -> ctypes.CDLL:
                                          sz, vp], i32),
             "spops_clip_grad_norm_workspace_size": ([i64, P(sz)], i32),
             "spops_clip_grad_norm": ([P(ClipTensor), i64, ctypes.c_double, vp, vp, sz, vp], i32),
+            "spops_mx4_quantize": ([vp, i32, i64, i64, i64, i64, vp, vp, vp], i32),
+            "spops_mx4_dequantize": ([P(Mx4Desc), vp, i32, i64, vp], i32),
+            "spops_mx4_matmul_workspace_size": ([P(Mx4Desc), i32, i32, i64, P(sz)], i32),
+            "spops_mx4_matmul": ([P(Mx4Desc), i32, vp, i32, i64, i64, vp, i64, vp, sz, vp], i32),
+            "spops_mx4_matmul4_workspace_size": ([P(Mx4Desc), i64, P(sz)], i32),
+            "spops_mx4_matmul4": ([P(Mx4Desc), P(Mx4Desc), vp, i32, i64, vp, sz, vp], i32),
+            "spops_dropout": ([vp, i32, i64, i64, i64, vp, i64, ctypes.c_double, ctypes.c_uint64,
+                               ctypes.c_uint64, vp, vp], i32),
         }
         for name, (args, res) in sigs.items():
             f = getattr(L, name)
@@ -774,3 +788,79 @@ def delta_spmv(D: DeltaMatrix, x: torch.Tensor, out_dtype: torch.dtype = torch.f
         D.m, D.n, _ptr(D.enc_offsets), D.entries, _ptr(D.codes), _ptr(D.values),
         _DT[D.values.dtype], _ptr(x), _ptr(out), _DT[out_dtype], _stream(x)))
     return out
+
+
+class Mx4Matrix:
+    """A matrix of 4-bit microscaled elements (the MXFP4 format): blocks of 32 along
+    the rows, each with a power of two as its scale.
+
+      codes   [rows, 16 ceil(cols / 32)] uint8, two elements a byte (even columns in the
+              low half); elements past the last column are zero
+      scales  [rows, ceil(cols / 32)] uint8, s stands for 2^(s - 127), 255 for NaN
+
+    mx4_quantize makes one; codes and scales of a checkpoint in this format can be
+    given as they are.  codes and scales are used, not copied."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
+        blocks = (cols + 31) // 32
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise ValueError("codes and scales must be uint8")
+        if cols < 1 or codes.dim() != 2 or codes.shape[0] < 1 or codes.shape[1] != 16 * blocks:
+            raise ValueError("codes must be rows x 16 ceil(cols / 32)")
+        if scales.shape != (codes.shape[0], blocks):
+            raise ValueError("scales must be rows x ceil(cols / 32)")
+        if not (codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError("codes and scales must be contiguous")
+        self.codes, self.scales = codes, scales
+        self.rows, self.cols = codes.shape[0], cols
+
+    @property
+    def shape(self) -> Tuple[int, int]:
+        return self.rows, self.cols
+
+    def __repr__(self) -> str:
+        return f"Mx4Matrix({self.rows} x {self.cols}, {self.codes.device})"
+
+
+def mx4_quantize(w: torch.Tensor) -> Mx4Matrix:
+    """w (rows x columns; f32, f16 or bf16) in 4-bit microscaled form, blocks along the
+    rows.  A block's scale is 2^(floor(log2(max |w|)) - 2), at least 2^-127 (1 for a
+    block of zeros); elements are rounded to nearest even and at most 6 times the scale.
+    A block that holds an infinity or a NaN becomes NaN.  Rows or columns of w have
+    unit stride: mx4_quantize(xt.t()) quantises activations (features x tokens) along
+    their features without a copy."""
+    codes, scales = _marshal().mx4_quantize(w)
+    return Mx4Matrix(codes, scales, w.shape[1])
+
+
+def mx4_dequantize(W: Mx4Matrix, dtype: torch.dtype = torch.float32,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values of W (f32 and bf16 hold every value, f16 those in its range)."""
+    return _marshal().mx4_dequantize(W.codes, W.scales, W.cols, _dtype_code(dtype), out)
+
+
+def mx4_matmul(W: Mx4Matrix, xt, transposed: bool = False,
+               out_dtype: Optional[torch.dtype] = None,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """W xt for activations xt (columns of W x tokens, unit stride along the tokens);
+    with `transposed` W^T xt for xt (rows of W x tokens).
+
+    xt is f32, f16 or bf16 and the result has its dtype; or xt is an Mx4Matrix (tokens
+    x columns of W, as mx4_quantize(xt.t()) gives it) and the result has `out_dtype`
+    (f32 by default).  Products are exact, sums f32, one rounding.  `out` overlaps no
+    input.  Not differentiable by itself: see mx4_linear."""
+    if isinstance(xt, Mx4Matrix):
+        if transposed:
+            raise ValueError("a transposed product takes activations that are not in four bits")
+        dtype = out_dtype or (torch.float32 if out is None else out.dtype)
+        return _marshal().mx4_matmul4(W.codes, W.scales, W.cols, xt.codes, xt.scales, xt.cols,
+                                      _dtype_code(dtype), out)
+    if out_dtype is not None and out_dtype != xt.dtype:
+        raise ValueError("the result has the dtype of xt")
+    return _marshal().mx4_matmul(W.codes, W.scales, W.cols, xt, bool(transposed), out)
+
+
+def _dtype_code(dtype: torch.dtype) -> int:
+    if dtype not in _DT:
+        raise ValueError("dtype must be float32, float16 or bfloat16")
+    return _DT[dtype]
