@@ -470,6 +470,10 @@ struct Mx4MatmulArgs {
   float* part;             // sums of the pieces of the inner size, [pieces][rows out][T]
   int32_t pieces, steps;   // pieces, and steps of 64 in each
 };
+// The product of few tokens (mx4_few.hip), not transposed; no workspace.  128 rows of x
+// are counted in 32 bits.
+constexpr int64_t kMx4FewLd = (int64_t)1 << 24;
+hipError_t launch_mx4_few(const Mx4MatmulArgs& a, int dtype, hipStream_t s);
 // Workspace bytes of a product.
 size_t mx4_matmul_bytes(const Mx4& W, int transposed, int dtype, int64_t T);
 hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, int transposed, int dtype, hipStream_t s);

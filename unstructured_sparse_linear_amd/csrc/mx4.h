@@ -69,6 +69,85 @@ __device__ __forceinline__ uint32_t mx4_encode(const float (&v)[8], float scale)
 
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
+// Eight values of x as they were loaded.
+template <typename T>
+struct Raw {
+  uint32_t w[2 * sizeof(T)];
+};
+
+template <typename T>
+__device__ __forceinline__ float raw_value(const Raw<T>& r, int i) {
+  if constexpr (sizeof(T) == 4)
+    return __uint_as_float(r.w[i]);
+  else
+    return i % 2 ? hi_f32(r.w[i / 2], (T*)nullptr) : lo_f32(r.w[i / 2], (T*)nullptr);
+}
+
+// Part p of eight values, as bf16 pairs: the upper 16 bits of the value, of what is
+// left, of what is left then.  An infinity or a NaN is all in the first part.
+template <typename T, int P>
+__device__ __forceinline__ void split(const Raw<T>& r, uint4 (&part)[P]) {
+  if constexpr (P == 1) {
+    part[0] = __builtin_bit_cast(uint4, r);
+  } else {
+    uint32_t w[P][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v[2] = {raw_value(r, 2 * i), raw_value(r, 2 * i + 1)};
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        uint32_t b[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          b[j] = __float_as_uint(v[j]);
+          // a NaN whose upper bits are an infinity's stays a NaN
+          if (p == 0 && magnitude(v[j]) > 0x7f800000u) b[j] |= 0x400000u;
+          const float rest = v[j] - __uint_as_float(b[j] & 0xffff0000u);
+          v[j] = magnitude(v[j]) >= 0x7f800000u ? 0.f : rest;
+        }
+        w[p][i] = __builtin_amdgcn_perm(b[1], b[0], 0x07060302u);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) part[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+  }
+}
+
+// Eight values of x from element `at` on, of which those from `end` on are not read.
+template <typename T>
+__device__ __forceinline__ Raw<T> load_until(const T* x, int64_t at, int64_t end) {
+  Raw<T> r;
+  if (at + 8 <= end) {
+    __builtin_memcpy(&r, x + at, sizeof(r));
+    return r;
+  }
+#pragma unroll
+  for (int i = 0; i < (int)(2 * sizeof(T)); ++i) r.w[i] = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (at + i >= end) break;
+    if constexpr (sizeof(T) == 4)
+      r.w[i] = __float_as_uint(x[at + i]);
+    else
+      r.w[i / 2] |= (uint32_t)bits16(x[at + i]) << (16 * (i % 2));
+  }
+  return r;
+}
+
+typedef __attribute__((address_space(3))) i16x4* Lds4;
+
+// Eight consecutive k of one column of a tile of rows of k, from the four lanes' rows
+// at `at` and four rows further: each group of 16 lanes reads four rows of 16 columns
+// and gets, in lane i, column i of them.
+__device__ __forceinline__ bf16x8_t turned(const char* at, int four_rows) {
+  const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)at);
+  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(at + four_rows));
+  struct {
+    i16x4 a, b;
+  } v = {lo, hi};
+  return __builtin_bit_cast(bf16x8_t, v);
+}
+
 // Workgroup index -> logical index, so that neighbours run on one XCD (workgroup b is
 // on XCD b mod 8).
 __device__ __forceinline__ uint32_t xcd_index(uint32_t b, uint32_t n) {

@@ -5,15 +5,18 @@
 //
 // An element of W times its scale has two significant bits, so bf16 holds it and its
 // product with a bf16 value is exact in f32.  x of f32 is cut into three bf16 parts
-// of eight bits each and x of f16 into two, which loses nothing (of f32 values under
-// 2^-109 the bits below 2^-133, the smallest bf16); every product is then exact and the
-// sums are f32.  Eight consecutive elements of the inner size (k)
+// of eight bits each, which loses nothing (of values under 2^-109 the bits below
+// 2^-133, the smallest bf16).  f16 holds the elements of the scales 104 to 140: with x
+// of f16 a workgroup first looks its scales through (32 KB of a tile of 256 x 4096) and
+// runs on f16, or, where others are among them, on bf16 with x in two parts.  So every
+// product is exact, and the sums are f32.  Eight consecutive elements of the inner size (k)
 // feed one half of v_mfma_f32_32x32x16_bf16 (row = lane % 32, half = lane / 32).
 //
 // A workgroup makes BM rows x BN tokens in steps of 64 k.  In a step, half h holds
 // the elements 32 h + 8 s + j of instruction s, so that the 16 bytes which a lane
 // loads of W are one block of one row, with one scale, for four instructions.
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "mx4.h"
@@ -23,140 +26,36 @@ namespace {
 
 constexpr int kStep = 64;
 
-template <typename T>
-struct Parts;
-template <>
-struct Parts<bf16_t> {
-  static constexpr int n = 1;
-};
-template <>
-struct Parts<_Float16> {
-  static constexpr int n = 2;
-};
-template <>
-struct Parts<float> {
-  static constexpr int n = 3;
-};
-
-// Eight values of x as they were loaded.
-template <typename T>
-struct Raw {
-  uint32_t w[2 * sizeof(T)];
-};
-
-template <typename T>
-__device__ __forceinline__ float raw_value(const Raw<T>& r, int i) {
-  if constexpr (sizeof(T) == 4)
-    return __uint_as_float(r.w[i]);
-  else
-    return i % 2 ? hi_f32(r.w[i / 2], (T*)nullptr) : lo_f32(r.w[i / 2], (T*)nullptr);
-}
-
-// Part p of eight values, as bf16 pairs: the upper 16 bits of the value, of what is
-// left, of what is left then.  An infinity or a NaN is all in the first part.
-template <typename T, int P>
-__device__ __forceinline__ void split(const Raw<T>& r, uint4 (&part)[P]) {
-  if constexpr (P == 1) {
-    part[0] = __builtin_bit_cast(uint4, r);
-  } else {
-    uint32_t w[P][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v[2] = {raw_value(r, 2 * i), raw_value(r, 2 * i + 1)};
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        uint32_t b[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          b[j] = __float_as_uint(v[j]);
-          // a NaN whose upper bits are an infinity's stays a NaN
-          if (p == 0 && magnitude(v[j]) > 0x7f800000u) b[j] |= 0x400000u;
-          const float rest = v[j] - __uint_as_float(b[j] & 0xffff0000u);
-          v[j] = magnitude(v[j]) >= 0x7f800000u ? 0.f : rest;
-        }
-        w[p][i] = __builtin_amdgcn_perm(b[1], b[0], 0x07060302u);
-      }
-    }
-#pragma unroll
-    for (int p = 0; p < P; ++p) part[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
-  }
-}
-
-// Eight values of row k from token t on; zeros past the matrix.
-template <typename T>
-__device__ __forceinline__ Raw<T> load_edge(const T* x, int64_t ldx, int64_t k, int64_t t,
-                                            int64_t K, int64_t tokens) {
-  Raw<T> r;
-#pragma unroll
-  for (int i = 0; i < (int)(2 * sizeof(T)); ++i) r.w[i] = 0u;
-  if (k >= K || t >= tokens) return r;
-  const T* const p = x + k * ldx + t;
-  if (t + 8 <= tokens) {
-    __builtin_memcpy(&r, p, sizeof(r));
-    return r;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (t + i >= tokens) break;
-    if constexpr (sizeof(T) == 4)
-      r.w[i] = __float_as_uint(p[i]);
-    else
-      r.w[i / 2] |= (uint32_t)bits16(p[i]) << (16 * (i % 2));
-  }
-  return r;
-}
-
-typedef __attribute__((address_space(3))) i16x4* Lds4;
-
-// Eight consecutive k of one column of a tile of rows of k, from the four lanes' rows
-// at `at` and four rows further: each group of 16 lanes reads four rows of 16 columns
-// and gets, in lane i, column i of them.
-__device__ __forceinline__ bf16x8_t turned(const char* at, int four_rows) {
-  const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)at);
-  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(at + four_rows));
-  struct {
-    i16x4 a, b;
-  } v = {lo, hi};
-  return __builtin_bit_cast(bf16x8_t, v);
-}
-
-// Block b of row r of W; past the matrix, zeros.
+// One block of W.
 struct Block {
   uint4 c;
   uint32_t s;
 };
-__device__ __forceinline__ Block load_block(const Mx4& W, int64_t nb, int64_t r, int64_t b) {
-  Block v{make_uint4(0u, 0u, 0u, 0u), 127u};
-  if (r < W.rows && b < nb) {
-    v.c = *(const uint4*)(W.codes + (r * nb + b) * 16);
-    v.s = W.scales[r * nb + b];
-  }
-  return v;
-}
 
-template <typename T, bool TR, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs a,
-                                                                   uint32_t tiles_m,
-                                                                   uint32_t tiles_n) {
-  constexpr int P = Parts<T>::n, kThreads = 64 * WM * WN;
+// One tile.  F: on f16.
+struct Tile {
+  int64_t m0, t0, first, last;  // rows, tokens, steps
+  uint32_t piece;
+};
+template <typename T, bool F>
+constexpr int kParts = sizeof(T) == 4 ? 3 : __is_same(T, _Float16) && !F ? 2 : 1;
+template <typename T, bool TR, int BM, int BN, bool F>
+constexpr int kTileBytes = 2 * kStep * 2 * (kParts<T, F> * BN + (TR ? BM : 0));
+
+template <typename T, bool TR, int BM, int BN, int WM, int WN, bool F>
+__device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile& tile, char* lds) {
+  constexpr int P = kParts<T, F>, kThreads = 64 * WM * WN;
   constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
   constexpr int kChunks = BN / 8, kRows = kThreads / kChunks, kPasses = kStep / kRows;
   constexpr int kXBytes = kStep * BN * 2, kWBytes = TR ? kStep * BM * 2 : 0;
   constexpr int kBlocks = BM / 32;  // of a row of W, transposed
   static_assert(!TR || kThreads == kStep * kBlocks, "a block a thread");
-  __shared__ __attribute__((aligned(16))) char lds[2 * (P * kXBytes + kWBytes)];
+  using E = std::conditional_t<F, _Float16, bf16_t>;
 
   const Mx4 W = a.W;
   const int64_t nb = (W.cols + kMx4Block - 1) / kMx4Block;
   const int64_t M = TR ? W.cols : W.rows, K = TR ? W.rows : W.cols;
-  const uint32_t index = xcd_index(blockIdx.x, gridDim.x);
-  const uint32_t tile = index % (tiles_m * tiles_n), piece = index / (tiles_m * tiles_n);
-  // four columns of tiles at a time, so that an XCD's workgroups share rows and columns
-  const uint32_t band = tile / (4 * tiles_m), in = tile % (4 * tiles_m);
-  const uint32_t wide = min(4u, tiles_n - 4 * band);
-  const int64_t m0 = (int64_t)(in / wide) * BM, t0 = (int64_t)(4 * band + in % wide) * BN;
-  const int64_t first = (int64_t)piece * a.steps;
-  const int64_t last = min(first + a.steps, (K + kStep - 1) / kStep);
+  const int64_t m0 = tile.m0, t0 = tile.t0, first = tile.first, last = tile.last;
 
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   const int wm = wave / WN, wn = wave % WN, half = lane / 32;
@@ -185,19 +84,48 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs
   Raw<T> xr[kPasses];
   Block wr[TR ? 1 : TM], wc[TR ? 1 : TM];
   const T* const x = (const T*)a.x;
-  const auto load = [&](int64_t step) {
+  const int64_t end = (K - 1) * a.ldx + a.T;  // of x
+  const int64_t xlane = xrow * a.ldx + 8 * xchunk;
+  // rows and blocks past the last of W read the last again: not transposed, they meet
+  // zeros of x or are not written; transposed, the other way round
+  const uint8_t *wcodes[TR ? 1 : TM], *wscales[TR ? 1 : TM];
+  const int64_t wb = min(m0 / kMx4Block + wblock, nb - 1);
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i)
-      xr[i] = load_edge(x, a.ldx, step * kStep + i * kRows + xrow, xt, K, a.T);
-    if constexpr (TR) {
-      wr[0] = load_block(W, nb, step * kStep + wrow, m0 / kMx4Block + wblock);
-    } else {
+  for (int m = 0; m < (TR ? 1 : TM); ++m) {
+    const int64_t r = TR ? 0 : min(m0 + (wm * TM + m) * 32 + lane % 32, W.rows - 1);
+    wcodes[m] = W.codes + (r * nb + (TR ? wb : 0)) * 16;
+    wscales[m] = W.scales + r * nb + (TR ? wb : 0);
+  }
+  // Nothing here looks at what a load brings, so that it comes while the step before is
+  // made.  Inside: every load of the step lies inside x (tokens past the last may hold
+  // anything, as their columns are not written).
+  const auto load = [&](int64_t step, auto inside) {
+    const int64_t at = step * kStep * a.ldx + t0;
 #pragma unroll
-      for (int m = 0; m < TM; ++m)
-        wr[m] = load_block(W, nb, m0 + (wm * TM + m) * 32 + lane % 32, 2 * step + half);
+    for (int i = 0; i < kPasses; ++i) {
+      if constexpr (decltype(inside)::value) {
+        __builtin_memcpy(&xr[i], x + at + i * kRows * a.ldx + xlane, sizeof(xr[i]));
+      } else {
+        const int64_t k = step * kStep + i * kRows + xrow, t = t0 + 8 * xchunk;
+        xr[i] = load_until(x, k * a.ldx + t, k < K && t < a.T ? end : 0);
+      }
+    }
+    const int64_t b = TR ? min(step * kStep + wrow, W.rows - 1) * nb : min(2 * step + half, nb - 1);
+#pragma unroll
+    for (int m = 0; m < (TR ? 1 : TM); ++m) {
+      wr[m].c = *(const uint4*)(wcodes[m] + b * 16);
+      wr[m].s = wscales[m][b];
     }
   };
-  const auto store = [&](int buffer) {
+  // the steps up to here lie inside
+  const int64_t room = end - BN - t0 - (kStep - 1) * a.ldx;
+  const int64_t inside_end = room < 0 ? 0 : room / (kStep * a.ldx) + 1;
+  const auto store = [&](int64_t step) {
+    const int buffer = (int)(step - first) & 1;
+    if (TR ? step * kStep + wrow >= W.rows : 2 * step + half >= nb) {
+#pragma unroll
+      for (int m = 0; m < (TR ? 1 : TM); ++m) wr[m].s = 127u;
+    }
     char* const xs = lds + buffer * P * kXBytes;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
@@ -214,7 +142,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs
       for (int i = 0; i < 4; ++i) {
         const int at = (4 * wblock + (i ^ ((wblock >> 2) & 3))) ^ ((wrow & 3) << 2);
         *(uint4*)(ws + (wrow * (BM / 8) + at) * 16) =
-            mx4_eight<bf16_t>(words[i], mx4_scale(wr[0].s));
+            mx4_eight<E>(words[i], mx4_scale(wr[0].s));
       }
     } else {
 #pragma unroll
@@ -230,15 +158,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.f;
 
-  if (first < last) {
-    load(first);
-    store(0);
-  }
-  __syncthreads();
-  for (int64_t step = first; step < last; ++step) {
+  const auto products = [&](int64_t step) {
     const int buffer = (int)(step - first) & 1;
-    const bool more = step + 1 < last;
-    if (more) load(step + 1);
     const char* const xs = lds + buffer * P * kXBytes;
     const char* const ws = lds + 2 * P * kXBytes + buffer * kWBytes;
 #pragma unroll
@@ -250,7 +171,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs
           wf[m] = turned(ws + wread[m] + s * 8 * BM * 2, 4 * BM * 2);
         } else {
           const uint32_t words[4] = {wc[m].c.x, wc[m].c.y, wc[m].c.z, wc[m].c.w};
-          wf[m] = __builtin_bit_cast(bf16x8_t, mx4_eight<bf16_t>(words[s], mx4_scale(wc[m].s)));
+          wf[m] = __builtin_bit_cast(bf16x8_t, mx4_eight<E>(words[s], mx4_scale(wc[m].s)));
         }
       }
 #pragma unroll
@@ -260,10 +181,36 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs
           const bf16x8_t xf = turned(xs + p * kXBytes + xread[n] + s * 8 * BN * 2, 4 * BN * 2);
 #pragma unroll
           for (int m = 0; m < TM; ++m)
-            acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf, wf[m], acc[m][n], 0, 0, 0);
+            acc[m][n] = F ? __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                                __builtin_bit_cast(f16x8_t, xf),
+                                __builtin_bit_cast(f16x8_t, wf[m]), acc[m][n], 0, 0, 0)
+                          : __builtin_amdgcn_mfma_f32_32x32x16_bf16(xf, wf[m], acc[m][n], 0, 0, 0);
         }
     }
-    if (more) store(buffer ^ 1);
+  };
+
+  // a step is made while the next one's loads come
+  int64_t step = first;
+  if (step < last) {
+    if (step < inside_end)
+      load(step, std::true_type());
+    else
+      load(step, std::false_type());
+    store(step);
+  }
+  __syncthreads();
+  for (; step + 1 < min(last, inside_end); ++step) {
+    load(step + 1, std::true_type());
+    // or the loads go below the products, and are waited for there
+    __builtin_amdgcn_sched_barrier(0);
+    products(step);
+    store(step + 1);
+    __syncthreads();
+  }
+  for (; step < last; ++step) {
+    if (step + 1 < last) load(step + 1, std::false_type());
+    products(step);
+    if (step + 1 < last) store(step + 1);
     __syncthreads();
   }
 
@@ -272,7 +219,66 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs
 #pragma unroll
     for (int n = 0; n < TN; ++n)
       mx4_write<T>(acc[m][n], m0 + (wm * TM + m) * 32, t0 + (wn * TN + n) * 32, M, a.T, a.out, a.ldo,
-                   a.part, piece);
+                   a.part, tile.piece);
+}
+
+// Whether any of `n` scales of `rows` rows from p on, `ld` apart, is one that f16 does
+// not hold.  Four to a word: those under 128 have to be 104 at least, the others 140 at
+// most.
+template <int THREADS>
+__device__ __forceinline__ bool wide_scales(const uint8_t* p, int64_t rows, int64_t n, int64_t ld) {
+  const auto outside = [](uint32_t w) {
+    const uint32_t low = (w | 0x80808080u) - 0x68686868u, high = (w | 0x80808080u) - 0x0d0d0d0du;
+    return ((~w & ~low) | (w & high)) & 0x80808080u;
+  };
+  uint32_t bad = 0;
+  const int64_t words = (n + 7) / 8;
+  for (int64_t i = threadIdx.x; i < rows * words; i += THREADS) {
+    const int64_t r = i / words, c = 8 * (i - r * words);
+    const uint8_t* const q = p + r * ld + c;
+    if (c + 8 <= n) {
+      uint32_t w[2];
+      __builtin_memcpy(w, q, 8);
+      bad |= outside(w[0]) | outside(w[1]);
+    } else {
+      for (int64_t j = 0; c + j < n; ++j) bad |= (uint32_t)q[j] - 104u > 36u;
+    }
+  }
+  return __syncthreads_or(bad != 0);
+}
+
+template <typename T, bool TR, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs a,
+                                                                   uint32_t tiles_m,
+                                                                   uint32_t tiles_n) {
+  constexpr bool H = __is_same(T, _Float16);
+  __shared__ __attribute__((aligned(16))) char
+      lds[std::max(kTileBytes<T, TR, BM, BN, H>, H ? kTileBytes<T, TR, BM, 128, false> : 0)];
+  const uint32_t index = xcd_index(blockIdx.x, gridDim.x);
+  const uint32_t at = index % (tiles_m * tiles_n), piece = index / (tiles_m * tiles_n);
+  // four columns of tiles at a time, so that an XCD's workgroups share rows and columns
+  const uint32_t band = at / (4 * tiles_m), in = at % (4 * tiles_m);
+  const uint32_t wide = min(4u, tiles_n - 4 * band);
+  const int64_t K = TR ? a.W.rows : a.W.cols;
+  Tile tile;
+  tile.m0 = (int64_t)(in / wide) * BM;
+  tile.t0 = (int64_t)(4 * band + in % wide) * BN;
+  tile.first = (int64_t)piece * a.steps;
+  tile.last = min(tile.first + a.steps, (K + kStep - 1) / kStep);
+  tile.piece = piece;
+  if constexpr (H) {
+    const int64_t nb = (a.W.cols + kMx4Block - 1) / kMx4Block;
+    const int64_t r0 = TR ? tile.first * kStep : tile.m0, b0 = TR ? tile.m0 / 32 : 2 * tile.first;
+    const int64_t rows = min(a.W.rows - r0, TR ? (tile.last - tile.first) * kStep : (int64_t)BM);
+    const int64_t n = min(nb - b0, TR ? (int64_t)BM / 32 : 2 * (tile.last - tile.first));
+    if (wide_scales<64 * WM * WN>(a.W.scales + r0 * nb + b0, rows, n, nb)) {
+      // in two parts x takes twice the room: 128 tokens at a time
+      for (int i = 0; i < BN / 128; ++i, tile.t0 += 128)
+        tile_product<T, TR, BM, 128, WM, WN, false>(a, tile, lds);
+      return;
+    }
+  }
+  tile_product<T, TR, BM, BN, WM, WN, H>(a, tile, lds);
 }
 
 struct Cut {
@@ -280,18 +286,21 @@ struct Cut {
   uint32_t tiles_m, tiles_n;
   int32_t pieces, steps;
 };
-// Large tiles where they fill half of the GPU; small ones cut along the inner size
-// until they fill it too, in pieces of at least four steps.
+// Large tiles (256 rows; transposed 256 tokens too) where they fill the GPU (4096 x 4096,
+// 2048 tokens: 76 us, 84 with small ones); small ones cut along the inner size until they
+// do, in pieces of at least four steps (4096 x 4096, 512 tokens: 47 us in two pieces, 53
+// in four, 256 tokens 37 in four, 45 in eight: the pieces are written and read again).
 Cut cut(const Mx4& W, int transposed, int dtype, int64_t T) {
   const int64_t M = transposed ? W.cols : W.rows, K = transposed ? W.rows : W.cols;
   const int64_t steps = cdiv(K, kStep);
   Cut c;
-  c.large = dtype != kF32 && cdiv(M, 256) * cdiv(T, dtype == kF16 ? 128 : 256) >= 128;
+  const int64_t wide = transposed ? 256 : 128;
+  c.large = dtype != kF32 && cdiv(M, 256) * cdiv(T, wide) >= (transposed ? 128 : 256);
   c.tiles_m = (uint32_t)cdiv(M, c.large ? 256 : 128);
-  c.tiles_n = (uint32_t)cdiv(T, c.large && dtype != kF16 ? 256 : 128);
+  c.tiles_n = (uint32_t)cdiv(T, c.large ? wide : 128);
   const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
-  int64_t pieces = c.large || tiles >= 256 ? 1 : std::min<int64_t>(512 / tiles, steps / 4);
-  pieces = std::max<int64_t>(pieces, 1);
+  const int64_t pieces =
+      c.large ? 1 : std::max<int64_t>(1, std::min<int64_t>(256 / tiles, steps / 4));
   c.steps = (int32_t)cdiv(steps, pieces);
   c.pieces = (int32_t)cdiv(steps, c.steps);
   return c;
@@ -301,18 +310,30 @@ template <typename T, bool TR>
 void launch(const Mx4MatmulArgs& a, const Cut& c, hipStream_t s) {
   const uint32_t blocks = c.tiles_m * c.tiles_n * (uint32_t)c.pieces;
   if constexpr (sizeof(T) == 2) {
-    constexpr int BN = Parts<T>::n == 1 ? 256 : 128;
     if (c.large) {
-      mx4_tile_kernel<T, TR, 256, BN, 4, 2><<<blocks, 512, 0, s>>>(a, c.tiles_m, c.tiles_n);
+      if constexpr (TR)
+        mx4_tile_kernel<T, TR, 256, 256, 4, 2><<<blocks, 512, 0, s>>>(a, c.tiles_m, c.tiles_n);
+      else
+        mx4_tile_kernel<T, TR, 256, 128, 4, 1><<<blocks, 256, 0, s>>>(a, c.tiles_m, c.tiles_n);
       return;
     }
   }
   mx4_tile_kernel<T, TR, 128, 128, 2, 2><<<blocks, 256, 0, s>>>(a, c.tiles_m, c.tiles_n);
 }
 
+// Up to this many tokens the kernel of few tokens is the faster.
+bool is_few(int transposed, int dtype, int64_t T) {
+  return !transposed && T <= (dtype == kF32 ? 32 : 128);
+}
+
 template <typename T>
 hipError_t matmul(Mx4MatmulArgs a, int transposed, int dtype, hipStream_t s) {
-  const Cut c = cut(a.W, transposed, dtype, a.T);
+  Cut c = cut(a.W, transposed, dtype, a.T);
+  if (is_few(transposed, dtype, a.T)) {
+    // rows of x further apart than that kernel counts: no workspace, so in one piece
+    c.pieces = 1;
+    c.steps = INT32_MAX;
+  }
   const int64_t M = transposed ? a.W.cols : a.W.rows;
   a.pieces = c.pieces;
   a.steps = c.steps;
@@ -328,12 +349,14 @@ hipError_t matmul(Mx4MatmulArgs a, int transposed, int dtype, hipStream_t s) {
 }  // namespace
 
 size_t mx4_matmul_bytes(const Mx4& W, int transposed, int dtype, int64_t T) {
+  if (is_few(transposed, dtype, T)) return 0;
   const Cut c = cut(W, transposed, dtype, T);
   if (c.pieces == 1) return 0;
   return (size_t)c.pieces * (size_t)(transposed ? W.cols : W.rows) * (size_t)T * 4;
 }
 
 hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, int transposed, int dtype, hipStream_t s) {
+  if (is_few(transposed, dtype, a.T) && a.ldx <= kMx4FewLd) return launch_mx4_few(a, dtype, s);
   if (dtype == kF32) return matmul<float>(a, transposed, dtype, s);
   if (dtype == kF16) return matmul<_Float16>(a, transposed, dtype, s);
   return matmul<bf16_t>(a, transposed, dtype, s);
