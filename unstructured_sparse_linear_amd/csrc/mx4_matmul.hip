@@ -13,8 +13,17 @@
 // feed one half of v_mfma_f32_32x32x16_bf16 (row = lane % 32, half = lane / 32).
 //
 // A workgroup makes BM rows x BN tokens in steps of 64 k.  In a step, half h holds
-// the elements 32 h + 8 s + j of instruction s, so that the 16 bytes which a lane
-// loads of W are one block of one row, with one scale, for four instructions.
+// the elements 32 h + 8 s + j of instruction s, so that 16 bytes of W are one block of
+// one row, with one scale, for four instructions.  x goes through shared memory as it
+// lies (rows of k) and is read turned; W goes through it as codes, two steps (64 bytes
+// a row) at a time, and is converted where it is used.  (Read by each lane for itself,
+// 16 bytes of 32 rows at a time, W took lines of the L1 four times over: 4096 x 4096,
+// 1024 tokens 65 us, so 52.)  W^T x converts W into shared memory and reads it turned.
+//
+// Bound by the matrix cores at the clock that their power leaves: with operands of
+// random bits they reach 1.65 PFLOP/s and no more.  8192 tokens, 4096 -> 11008, bf16:
+// 651 to 690 us, 1.07 to 1.13 PFLOP/s (a library's dense bf16 product of that size
+// 1.05); gradient of 4096 tokens, 4096 x 4096: 130 us, 1.05.
 #include <algorithm>
 #include <type_traits>
 
@@ -26,43 +35,44 @@ namespace {
 
 constexpr int kStep = 64;
 
-// One block of W.
-struct Block {
-  uint4 c;
-  uint32_t s;
-};
-
-// One tile.  F: on f16.
+// One tile, and the steps of its inner size.
 struct Tile {
-  int64_t m0, t0, first, last;  // rows, tokens, steps
+  int64_t m0, t0, first, last;
   uint32_t piece;
 };
+// F: on f16.  SB: x in a single buffer.
 template <typename T, bool F>
 constexpr int kParts = sizeof(T) == 4 ? 3 : __is_same(T, _Float16) && !F ? 2 : 1;
-template <typename T, bool TR, int BM, int BN, bool F>
-constexpr int kTileBytes = 2 * kStep * 2 * (kParts<T, F> * BN + (TR ? BM : 0));
+template <typename T, bool TR, int BM, int BN, bool F, bool SB>
+constexpr int kTileBytes = (SB ? 1 : 2) * kParts<T, F> * BN * 2 * kStep +
+                           2 * BM * (TR ? 2 * kStep : 4 * 16 + 4);
 
-template <typename T, bool TR, int BM, int BN, int WM, int WN, bool F>
+template <typename T, bool TR, int BM, int BN, int WM, int WN, bool F, bool SB>
 __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile& tile, char* lds) {
   constexpr int P = kParts<T, F>, kThreads = 64 * WM * WN;
   constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
   constexpr int kChunks = BN / 8, kRows = kThreads / kChunks, kPasses = kStep / kRows;
-  constexpr int kXBytes = kStep * BN * 2, kWBytes = TR ? kStep * BM * 2 : 0;
+  constexpr int kXBytes = kStep * BN * 2;
   constexpr int kBlocks = BM / 32;  // of a row of W, transposed
+  // W in shared memory: transposed a step as 16-bit values, otherwise two steps as they
+  // are, 64 bytes of codes and 4 scales a row
+  constexpr int kWBytes = TR ? kStep * BM * 2 : BM * 68;
+  constexpr int kW = TR ? 1 : BM * 4 / kThreads;  // loads of codes
   static_assert(!TR || kThreads == kStep * kBlocks, "a block a thread");
+  static_assert(TR || (BM * 4 % kThreads == 0 && BM <= kThreads), "whole loads");
   using E = std::conditional_t<F, _Float16, bf16_t>;
 
   const Mx4 W = a.W;
   const int64_t nb = (W.cols + kMx4Block - 1) / kMx4Block;
   const int64_t M = TR ? W.cols : W.rows, K = TR ? W.rows : W.cols;
   const int64_t m0 = tile.m0, t0 = tile.t0, first = tile.first, last = tile.last;
+  char* const wlds = lds + (SB ? 1 : 2) * P * kXBytes;
 
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   const int wm = wave / WN, wn = wave % WN, half = lane / 32;
   // x is stored with the 64-byte groups of a row turned by the row, so that the four
   // rows that are read at once lie in different banks
   const int xrow = tid / kChunks, xchunk = tid % kChunks;
-  const int64_t xt = t0 + 8 * xchunk;
   const int xstore = (xrow * kChunks + (xchunk ^ ((xrow & 3) << 2))) * 16;
   const int l16 = lane % 16, sub = (lane / 16) % 2;
   const int chunk = 2 * sub + (l16 % 4) / 2, byte = 8 * (l16 & 1), trow = 32 * half + l16 / 4;
@@ -70,36 +80,26 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
 #pragma unroll
   for (int n = 0; n < TN; ++n)
     xread[n] = (trow * kChunks + ((4 * (wn * TN + n) + chunk) ^ ((l16 / 4) << 2))) * 16 + byte;
-  // transposed, W is stored as bf16 in the same way, a block's four pieces turned by
-  // the block
+  // transposed, W is stored in the same way, a block's four pieces turned by the block;
+  // otherwise a row's four blocks are turned by the row, for the 16 rows read at once
   const int wrow = tid / kBlocks, wblock = tid % kBlocks;
   int wread[TM];
 #pragma unroll
   for (int m = 0; m < TM; ++m) {
-    const int b = wm * TM + m;
-    wread[m] = (trow * (BM / 8) + ((4 * b + (chunk ^ ((b >> 2) & 3))) ^ ((l16 / 4) << 2))) * 16 +
-               byte;
+    const int b = wm * TM + m, r = 32 * b + lane % 32;
+    wread[m] = TR ? (trow * (BM / 8) + ((4 * b + (chunk ^ ((b >> 2) & 3))) ^ ((l16 / 4) << 2))) *
+                            16 + byte
+                  : r * 64 + 16 * (half ^ ((r >> 2) & 3));
   }
 
-  Raw<T> xr[kPasses];
-  Block wr[TR ? 1 : TM], wc[TR ? 1 : TM];
   const T* const x = (const T*)a.x;
   const int64_t end = (K - 1) * a.ldx + a.T;  // of x
   const int64_t xlane = xrow * a.ldx + 8 * xchunk;
-  // rows and blocks past the last of W read the last again: not transposed, they meet
-  // zeros of x or are not written; transposed, the other way round
-  const uint8_t *wcodes[TR ? 1 : TM], *wscales[TR ? 1 : TM];
-  const int64_t wb = min(m0 / kMx4Block + wblock, nb - 1);
-#pragma unroll
-  for (int m = 0; m < (TR ? 1 : TM); ++m) {
-    const int64_t r = TR ? 0 : min(m0 + (wm * TM + m) * 32 + lane % 32, W.rows - 1);
-    wcodes[m] = W.codes + (r * nb + (TR ? wb : 0)) * 16;
-    wscales[m] = W.scales + r * nb + (TR ? wb : 0);
-  }
-  // Nothing here looks at what a load brings, so that it comes while the step before is
-  // made.  Inside: every load of the step lies inside x (tokens past the last may hold
-  // anything, as their columns are not written).
-  const auto load = [&](int64_t step, auto inside) {
+  Raw<T> xr[kPasses];
+  // Nothing in a load looks at what another brings, so that they come while the step
+  // before is made.  Inside: every load of the step lies inside x (tokens past the last
+  // may hold anything, as their columns are not written).
+  const auto load_x = [&](int64_t step, auto inside) {
     const int64_t at = step * kStep * a.ldx + t0;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
@@ -110,23 +110,18 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
         xr[i] = load_until(x, k * a.ldx + t, k < K && t < a.T ? end : 0);
       }
     }
-    const int64_t b = TR ? min(step * kStep + wrow, W.rows - 1) * nb : min(2 * step + half, nb - 1);
-#pragma unroll
-    for (int m = 0; m < (TR ? 1 : TM); ++m) {
-      wr[m].c = *(const uint4*)(wcodes[m] + b * 16);
-      wr[m].s = wscales[m][b];
-    }
   };
   // the steps up to here lie inside
   const int64_t room = end - BN - t0 - (kStep - 1) * a.ldx;
   const int64_t inside_end = room < 0 ? 0 : room / (kStep * a.ldx) + 1;
-  const auto store = [&](int64_t step) {
-    const int buffer = (int)(step - first) & 1;
-    if (TR ? step * kStep + wrow >= W.rows : 2 * step + half >= nb) {
-#pragma unroll
-      for (int m = 0; m < (TR ? 1 : TM); ++m) wr[m].s = 127u;
-    }
-    char* const xs = lds + buffer * P * kXBytes;
+  const auto load_x_any = [&](int64_t step) {
+    if (step < inside_end)
+      load_x(step, std::true_type());
+    else
+      load_x(step, std::false_type());
+  };
+  const auto store_x = [&](int64_t step) {
+    char* const xs = lds + (SB ? 0 : (int)(step - first) & 1) * P * kXBytes;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       uint4 part[P];
@@ -135,18 +130,63 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
       for (int p = 0; p < P; ++p)
         *(uint4*)(xs + p * kXBytes + xstore + i * kRows * kChunks * 16) = part[p];
     }
+  };
+
+  // W of one step (transposed) or of two.  Rows and blocks past the last read the last
+  // again: what they give meets zeros of x, for which scales past the inner size are
+  // made finite, or is not written.
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 wr[kW];
+  uint32_t ws = 0;
+  const auto load_w = [&](int64_t step, auto inside) {
+    constexpr bool I = decltype(inside)::value;
     if constexpr (TR) {
-      char* const ws = lds + 2 * P * kXBytes + buffer * kWBytes;
-      const uint32_t words[4] = {wr[0].c.x, wr[0].c.y, wr[0].c.z, wr[0].c.w};
+      const int64_t r = step * kStep + wrow;
+      const int64_t at = (I ? r : min(r, W.rows - 1)) * nb + min(m0 / kMx4Block + wblock, nb - 1);
+      wr[0] = *(const u32x4*)(W.codes + at * 16);
+      ws = W.scales[at];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kW; ++i) {
+        const int id = tid + i * kThreads;
+        const int64_t r = min(m0 + id / 4, W.rows - 1), b = 2 * step + id % 4;
+        wr[i] = *(const u32x4*)(W.codes + (r * nb + (I ? b : min(b, nb - 1))) * 16);
+      }
+      if (BM == kThreads || tid < BM) {
+        const uint8_t* const p = W.scales + min(m0 + tid, W.rows - 1) * nb + 2 * step;
+        if constexpr (I) {
+          typedef uint32_t word __attribute__((aligned(1)));
+          ws = *(const word*)p;
+        } else {
+          uint32_t w = 0x7f7f7f7fu;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (2 * step + i < nb) w = (w & ~(0xffu << (8 * i))) | ((uint32_t)p[i] << (8 * i));
+          ws = w;
+        }
+      }
+    }
+  };
+  // the steps up to here lie inside x and W, and so do the loads of W that go with them
+  const int64_t hot_end =
+      min(min(last, inside_end), TR ? last : nb < 4 ? 0 : (nb - 4) / 2 + 1);
+  const auto store_w = [&](int64_t step) {
+    char* const to = wlds + ((int)(step - first) >> (TR ? 0 : 1) & 1) * kWBytes;
+    if constexpr (TR) {
+      const float scale = mx4_scale(step * kStep + wrow < W.rows ? ws : 127u);
+      const uint32_t words[4] = {wr[0][0], wr[0][1], wr[0][2], wr[0][3]};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int at = (4 * wblock + (i ^ ((wblock >> 2) & 3))) ^ ((wrow & 3) << 2);
-        *(uint4*)(ws + (wrow * (BM / 8) + at) * 16) =
-            mx4_eight<E>(words[i], mx4_scale(wr[0].s));
+        *(uint4*)(to + (wrow * (BM / 8) + at) * 16) = mx4_eight<E>(words[i], scale);
       }
     } else {
 #pragma unroll
-      for (int m = 0; m < TM; ++m) wc[m] = wr[m];
+      for (int i = 0; i < kW; ++i) {
+        const int id = tid + i * kThreads, r = id / 4;
+        *(u32x4*)(to + r * 64 + 16 * ((id % 4) ^ ((r >> 2) & 3))) = wr[i];
+      }
+      if (BM == kThreads || tid < BM) *(uint32_t*)(to + BM * 64 + tid * 4) = ws;
     }
   };
 
@@ -158,20 +198,33 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.f;
 
-  const auto products = [&](int64_t step) {
-    const int buffer = (int)(step - first) & 1;
-    const char* const xs = lds + buffer * P * kXBytes;
-    const char* const ws = lds + 2 * P * kXBytes + buffer * kWBytes;
+  // One step; U: whether it is the second of a pair.
+  const auto products = [&](int64_t step, auto second) {
+    constexpr int U = decltype(second)::value;
+    const int at = (int)(step - first);
+    const char* const xs = lds + (SB ? 0 : at & 1) * P * kXBytes;
+    const char* const wl = wlds + (TR ? at & 1 : at >> 1 & 1) * kWBytes;
+    uint4 wc[TM];
+    float scale[TM];
+    if constexpr (!TR) {
+#pragma unroll
+      for (int m = 0; m < TM; ++m) {
+        wc[m] = *(const uint4*)(wl + (wread[m] ^ (32 * U)));
+        const uint32_t s4 =
+            *(const uint32_t*)(wl + BM * 64 + ((wm * TM + m) * 32 + lane % 32) * 4);
+        scale[m] = mx4_scale((s4 >> (16 * U + 8 * half)) & 0xffu);
+      }
+    }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       bf16x8_t wf[TM];
 #pragma unroll
       for (int m = 0; m < TM; ++m) {
         if constexpr (TR) {
-          wf[m] = turned(ws + wread[m] + s * 8 * BM * 2, 4 * BM * 2);
+          wf[m] = turned(wl + wread[m] + s * 8 * BM * 2, 4 * BM * 2);
         } else {
-          const uint32_t words[4] = {wc[m].c.x, wc[m].c.y, wc[m].c.z, wc[m].c.w};
-          wf[m] = __builtin_bit_cast(bf16x8_t, mx4_eight<E>(words[s], mx4_scale(wc[m].s)));
+          const uint32_t words[4] = {wc[m].x, wc[m].y, wc[m].z, wc[m].w};
+          wf[m] = __builtin_bit_cast(bf16x8_t, mx4_eight<E>(words[s], scale[m]));
         }
       }
 #pragma unroll
@@ -189,28 +242,52 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
     }
   };
 
-  // a step is made while the next one's loads come
+  // A step is made while the next one's loads come.  (The scheduling barriers keep the
+  // loads before the products: below them they would be waited for.)
   int64_t step = first;
   if (step < last) {
-    if (step < inside_end)
-      load(step, std::true_type());
-    else
-      load(step, std::false_type());
-    store(step);
+    load_w(step, std::false_type());
+    load_x_any(step);
+    store_w(step);
+    store_x(step);
   }
   __syncthreads();
-  for (; step + 1 < min(last, inside_end); ++step) {
-    load(step + 1, std::true_type());
-    // or the loads go below the products, and are waited for there
-    __builtin_amdgcn_sched_barrier(0);
-    products(step);
-    store(step + 1);
-    __syncthreads();
+  if constexpr (!SB) {
+    for (; step + 2 < hot_end; step += 2) {
+      load_x(step + 1, std::true_type());
+      load_w(step + (TR ? 1 : 2), std::true_type());
+      __builtin_amdgcn_sched_barrier(0);
+      products(step, std::integral_constant<int, 0>());
+      store_x(step + 1);
+      if constexpr (TR) store_w(step + 1);
+      __syncthreads();
+      load_x(step + 2, std::true_type());
+      if constexpr (TR) load_w(step + 2, std::true_type());
+      __builtin_amdgcn_sched_barrier(0);
+      products(step + 1, std::integral_constant<int, 1>());
+      store_x(step + 2);
+      store_w(step + 2);
+      __syncthreads();
+    }
   }
-  for (; step < last; ++step) {
-    if (step + 1 < last) load(step + 1, std::false_type());
-    products(step);
-    if (step + 1 < last) store(step + 1);
+  const auto next = [&](int64_t to, bool w) {
+    if (to >= last) return;
+    if (SB) load_x_any(to);
+    if (SB) __syncthreads();
+    store_x(to);
+    if (w) store_w(to);
+  };
+  for (; step < last; step += 2) {
+    if (!SB && step + 1 < last) load_x_any(step + 1);
+    if (step + 1 < last) load_w(step + (TR ? 1 : 2), std::false_type());
+    products(step, std::integral_constant<int, 0>());
+    next(step + 1, TR);
+    __syncthreads();
+    if (step + 1 >= last) break;
+    if (!SB && step + 2 < last) load_x_any(step + 2);
+    if (TR && step + 2 < last) load_w(step + 2, std::false_type());
+    products(step + 1, std::integral_constant<int, 1>());
+    next(step + 2, true);
     __syncthreads();
   }
 
@@ -253,7 +330,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs
                                                                    uint32_t tiles_n) {
   constexpr bool H = __is_same(T, _Float16);
   __shared__ __attribute__((aligned(16))) char
-      lds[std::max(kTileBytes<T, TR, BM, BN, H>, H ? kTileBytes<T, TR, BM, 128, false> : 0)];
+      lds[std::max(kTileBytes<T, TR, BM, BN, H, false>,
+                   H ? kTileBytes<T, TR, BM, 128, false, true> : 0)];
   const uint32_t index = xcd_index(blockIdx.x, gridDim.x);
   const uint32_t at = index % (tiles_m * tiles_n), piece = index / (tiles_m * tiles_n);
   // four columns of tiles at a time, so that an XCD's workgroups share rows and columns
@@ -274,11 +352,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs
     if (wide_scales<64 * WM * WN>(a.W.scales + r0 * nb + b0, rows, n, nb)) {
       // in two parts x takes twice the room: 128 tokens at a time
       for (int i = 0; i < BN / 128; ++i, tile.t0 += 128)
-        tile_product<T, TR, BM, 128, WM, WN, false>(a, tile, lds);
+        tile_product<T, TR, BM, 128, WM, WN, false, true>(a, tile, lds);
       return;
     }
   }
-  tile_product<T, TR, BM, BN, WM, WN, H>(a, tile, lds);
+  tile_product<T, TR, BM, BN, WM, WN, H, false>(a, tile, lds);
 }
 
 struct Cut {
