@@ -155,37 +155,60 @@ __device__ __forceinline__ uint32_t xcd_index(uint32_t b, uint32_t n) {
   return q * each + min(q, more) + b / 8;
 }
 
-// A 32 x 32 result of v_mfma_f32_32x32x* whose rows are tokens and whose columns are
-// rows of W: a lane holds row r0 + lane % 32 and runs of four tokens.  To `out`
-// ([M][tokens], ldo), or, where the inner size is cut, to piece `piece` of `part`.
-template <typename T>
-__device__ __forceinline__ void mx4_write(const f32x16& acc, int64_t r0, int64_t t0, int64_t M,
-                                          int64_t tokens, void* out, int64_t ldo, float* part,
-                                          uint32_t piece) {
+// A wave's memory is written before it is read by other lanes, and read before it is
+// written again.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Shared memory a wave needs for mx4_write.
+constexpr int kWriteBytes = 32 * (256 + 16);
+
+// TN results of v_mfma_f32_32x32x* side by side whose rows are tokens and whose columns
+// are rows of W: a lane holds row r0 + lane % 32 and runs of four tokens.  They go
+// through shared memory, up to 256 bytes of a row at a time, so that a row's tokens are
+// stored 16 bytes a lane side by side (stored as they are held, 8 bytes of 32 rows at a
+// time, they took 25 of 80 us of 4096^2 in four bits on 4096 tokens).
+template <typename E, int TN>
+__device__ __forceinline__ void mx4_write(const f32x16 (&acc)[TN], char* lds, int64_t r0,
+                                          int64_t t0, int64_t M, int64_t tokens, E* out,
+                                          int64_t ld) {
+  constexpr int N = TN * sizeof(E) < 8 ? TN : 8 / sizeof(E);  // results at a time
+  constexpr int kRow = N * 32 * sizeof(E) + 16, kEach = 16 / sizeof(E);
+  constexpr int kLanes = N * 32 / kEach, kRows = 64 / kLanes;
   const int lane = lane_id();
-  const int64_t r = r0 + lane % 32;
-  if (r >= M) return;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int64_t t = t0 + 8 * g + 4 * (lane / 32);
-    if (part) {
-      float* const p = part + ((int64_t)piece * M + r) * tokens + t;
+  for (int n0 = 0; n0 < TN; n0 += N) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (t + i < tokens) p[i] = acc[4 * g + i];
-    } else {
-      T* const p = (T*)out + r * ldo + t;
-      T v[4];
+    for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = from_f32<T>(acc[4 * g + i]);
-      if (t + 4 <= tokens) {
-        __builtin_memcpy(p, v, sizeof(v));
+      for (int g = 0; g < 4; ++g) {
+        E v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = from_f32<E>(acc[n0 + n][4 * g + i]);
+        char* const to = lds + lane % 32 * kRow + (32 * n + 8 * g + 4 * (lane / 32)) * sizeof(E);
+        __builtin_memcpy(__builtin_assume_aligned(to, 4 * sizeof(E)), v, sizeof(v));
+      }
+    wave_fence();
+    const int64_t t = t0 + 32 * n0 + lane % kLanes * kEach;
+#pragma unroll
+    for (int i = 0; i < 32 / kRows; ++i) {
+      const int r = i * kRows + lane / kLanes;
+      if (r0 + r >= M || t >= tokens) continue;
+      E v[kEach];
+      __builtin_memcpy(v, __builtin_assume_aligned(lds + r * kRow + lane % kLanes * 16, 16), 16);
+      E* const p = out + (r0 + r) * ld + t;
+      if (t + kEach <= tokens) {
+        __builtin_memcpy(p, v, 16);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (t + i < tokens) p[i] = v[i];
+        for (int j = 0; j < kEach; ++j)
+          if (t + j < tokens) p[j] = v[j];
       }
     }
+    wave_fence();
   }
 }
 

@@ -228,9 +228,7 @@ __global__ __launch_bounds__(64 * kWaves) void mx4_few_kernel(Mx4MatmulArgs a) {
             *(uint4*)(xs + p * kPart + (first_row / 32) * kGroup +
                       (first_row % 32 + xrow) * kRow + 16 * xchunk) = part[p];
         }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        wave_fence();
         load_x(i + 1 < kAhead ? slab_at(first, i + 1) : slab_at(then, 0), raw[0]);
       }
       uint32_t scale[RT];
@@ -257,9 +255,7 @@ __global__ __launch_bounds__(64 * kWaves) void mx4_few_kernel(Mx4MatmulArgs a) {
         if (kXAhead == 1)
           load_x(i + 1 < kAhead ? slab_at(first, i + 1) : slab_at(then, 0), raw[0]);
       } else {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        wave_fence();
       }
     }
     if (more) {

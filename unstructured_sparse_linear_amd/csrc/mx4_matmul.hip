@@ -59,6 +59,7 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
   constexpr int kWBytes = TR ? kStep * BM * 2 : BM * 68;
   constexpr int kW = TR ? 1 : BM * 4 / kThreads;  // loads of codes
   static_assert(!TR || kThreads == kStep * kBlocks, "a block a thread");
+  static_assert(WM * WN * kWriteBytes <= kTileBytes<T, TR, BM, BN, F, SB>, "room for output");
   static_assert(TR || (BM * 4 % kThreads == 0 && BM <= kThreads), "whole loads");
   using E = std::conditional_t<F, _Float16, bf16_t>;
 
@@ -291,12 +292,16 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
     __syncthreads();
   }
 
+  // (every wave is past the last step's barrier)
+  char* const mine = lds + wave * kWriteBytes;
 #pragma unroll
-  for (int m = 0; m < TM; ++m)
-#pragma unroll
-    for (int n = 0; n < TN; ++n)
-      mx4_write<T>(acc[m][n], m0 + (wm * TM + m) * 32, t0 + (wn * TN + n) * 32, M, a.T, a.out, a.ldo,
-                   a.part, tile.piece);
+  for (int m = 0; m < TM; ++m) {
+    const int64_t r0 = m0 + (wm * TM + m) * 32, tw = t0 + wn * TN * 32;
+    if (a.part)
+      mx4_write(acc[m], mine, r0, tw, M, a.T, a.part + (int64_t)tile.piece * M * a.T, a.T);
+    else
+      mx4_write(acc[m], mine, r0, tw, M, a.T, (T*)a.out, a.ldo);
+  }
 }
 
 // Whether any of `n` scales of `rows` rows from p on, `ld` apart, is one that f16 does

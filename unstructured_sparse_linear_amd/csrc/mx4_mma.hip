@@ -5,6 +5,7 @@
 // one row (row = lane % 32, block = lane / 32) and its scale byte.  Products are
 // exact, the sums f32.
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "mx4.h"
@@ -13,8 +14,10 @@ namespace spops {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kStep = 128;  // k of a step: four blocks
+constexpr int kStep = 256;           // k of a step: eight blocks, 128 bytes of a row
+constexpr int kBlocks = kStep / 32;
 
 struct Args {
   Mx4 W, X;
@@ -24,40 +27,23 @@ struct Args {
   int32_t steps;
 };
 
-__device__ __forceinline__ i32x8 operand(const uint4& c) {
-  i32x8 v = {(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
+__device__ __forceinline__ i32x8 operand(const u32x4& c) {
+  i32x8 v = {(int)c[0], (int)c[1], (int)c[2], (int)c[3], 0, 0, 0, 0};
   return v;
-}
-
-// Block b of row r; past the matrix, zeros.
-__device__ __forceinline__ uint4 load_codes(const Mx4& A, int64_t nb, int64_t r, int64_t b) {
-  if (r >= A.rows || b >= nb) return make_uint4(0u, 0u, 0u, 0u);
-  return *(const uint4*)(A.codes + (r * nb + b) * 16);
-}
-// Scales of four blocks from b on; past the matrix, ones.
-__device__ __forceinline__ uint32_t load_scales(const Mx4& A, int64_t nb, int64_t r, int64_t b) {
-  uint32_t w = 0x7f7f7f7fu;
-  if (r >= A.rows) return w;
-  const uint8_t* const p = A.scales + r * nb + b;
-  if (b + 4 <= nb) {
-    __builtin_memcpy(&w, p, 4);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (b + i < nb) w = (w & ~(0xffu << (8 * i))) | ((uint32_t)p[i] << (8 * i));
-  }
-  return w;
 }
 
 // BM rows x BN tokens; WM x WN waves.
 template <typename T, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_mma_kernel(Args a, uint32_t tiles_m,
                                                                   uint32_t tiles_n) {
-  constexpr int kThreads = 64 * WM * WN, kRows = kThreads / 4;
+  constexpr int kThreads = 64 * WM * WN, kRows = BM + BN, kLoads = kRows * kBlocks / kThreads;
   constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
-  static_assert(BM % kRows == 0 && BN % kRows == 0 && BM + BN <= kThreads, "whole passes");
-  constexpr int kStage = (BM + BN) * 68;  // codes, then scales
-  __shared__ __attribute__((aligned(16))) char lds[2 * kStage];
+  static_assert(kRows == kThreads && BM % 64 == 0, "a row of scales a thread, waves of one matrix");
+  constexpr int kCodes = kRows * 128, kScales = kRows * 16;
+  static_assert(BM * kBlocks % kThreads == 0 &&
+                    WM * WN * kWriteBytes <= 2 * (kCodes + kScales),
+                "whole loads of each matrix, room for the output");
+  __shared__ __attribute__((aligned(16))) char lds[2 * (kCodes + kScales)];
 
   const int64_t nb = (a.W.cols + kMx4Block - 1) / kMx4Block;
   const uint32_t index = xcd_index(blockIdx.x, gridDim.x);
@@ -66,40 +52,69 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_mma_kernel(Args a, uint32
   const uint32_t wide = min(4u, tiles_n - 4 * band);
   const int64_t m0 = (int64_t)(in / wide) * BM, t0 = (int64_t)(4 * band + in % wide) * BN;
   const int64_t first = (int64_t)piece * a.steps;
-  const int64_t last = min(first + a.steps, (a.W.cols + kStep - 1) / kStep);
+  const int64_t last = min(first + a.steps, (nb + kBlocks - 1) / kBlocks);
 
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   const int wm = wave / WN, wn = wave % WN, half = lane / 32;
-  // rows of four blocks, turned by the row, so that 16 rows read at once lie in
+  // a row's eight blocks are turned by the row, so that 16 rows read at once lie in
   // different banks
-  const int srow = tid / 4, sblock = tid % 4;
-  uint4 wr[BM / kRows], xr[BN / kRows];
-  uint32_t sr = 0;
+  int wread[TM], xread[TN];
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+    const int r = (wm * TM + m) * 32 + lane % 32;
+    wread[m] = r * 128 + 16 * (half ^ ((r >> 1) & 7));
+  }
+#pragma unroll
+  for (int n = 0; n < TN; ++n) {
+    const int r = BM + (wn * TN + n) * 32 + lane % 32;
+    xread[n] = r * 128 + 16 * (half ^ ((r >> 1) & 7));
+  }
+
+  // Rows and blocks past the last read it again: what the rows give is not written, and
+  // the blocks are stored as zeros of scale one.
+  const int block = tid % kBlocks;
+  u32x4 codes[kLoads], scales;
   const auto load = [&](int64_t step) {
+    const int64_t b = min(kBlocks * step + block, nb - 1);
 #pragma unroll
-    for (int i = 0; i < BM / kRows; ++i)
-      wr[i] = load_codes(a.W, nb, m0 + i * kRows + srow, 4 * step + sblock);
-#pragma unroll
-    for (int i = 0; i < BN / kRows; ++i)
-      xr[i] = load_codes(a.X, nb, t0 + i * kRows + srow, 4 * step + sblock);
-    if (tid < BM)
-      sr = load_scales(a.W, nb, m0 + tid, 4 * step);
-    else if (tid < BM + BN)
-      sr = load_scales(a.X, nb, t0 + tid - BM, 4 * step);
+    for (int i = 0; i < kLoads; ++i) {
+      const Mx4& A = i < BM * kBlocks / kThreads ? a.W : a.X;
+      const int r = (tid + i * kThreads) / kBlocks;
+      const int64_t row = min(i < BM * kBlocks / kThreads ? m0 + r : t0 + r - BM, A.rows - 1);
+      codes[i] = *(const u32x4*)(A.codes + (row * nb + b) * 16);
+    }
   };
-  const auto store = [&](int buffer) {
-    char* const s = lds + buffer * kStage;
+  // scales of two steps
+  const Mx4& mine_of = tid < BM ? a.W : a.X;
+  const uint8_t* const my_scales =
+      mine_of.scales + min(tid < BM ? m0 + tid : t0 + tid - BM, mine_of.rows - 1) * nb;
+  const auto load_scales = [&](int64_t step) {
+    const int64_t b = kBlocks * step;
+    if (b + 16 <= nb) {
+      typedef uint32_t bytes16 __attribute__((ext_vector_type(4), aligned(1)));
+      scales = *(const bytes16*)(my_scales + b);
+    } else {
 #pragma unroll
-    for (int i = 0; i < BM / kRows; ++i) {
-      const int r = i * kRows + srow;
-      *(uint4*)(s + r * 64 + 16 * (sblock ^ ((r >> 2) & 3))) = wr[i];
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w = 0x7f7f7f7fu;
+#pragma unroll 1
+        for (int j = 0; j < 4 && b + 4 * i + j < nb; ++j)
+          w = (w & ~(0xffu << (8 * j))) | ((uint32_t)my_scales[b + 4 * i + j] << (8 * j));
+        scales[i] = w;
+      }
     }
+  };
+  const auto store = [&](int64_t step) {
+    char* const to = lds + ((int)(step - first) & 1) * kCodes;
+    const uint32_t keep = kBlocks * step + block < nb ? ~0u : 0u;
 #pragma unroll
-    for (int i = 0; i < BN / kRows; ++i) {
-      const int r = BM + i * kRows + srow;
-      *(uint4*)(s + r * 64 + 16 * (sblock ^ ((r >> 2) & 3))) = xr[i];
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = (tid + i * kThreads) / kBlocks;
+      *(u32x4*)(to + r * 128 + 16 * (block ^ ((r >> 1) & 7))) = codes[i] & keep;
     }
-    if (tid < BM + BN) *(uint32_t*)(s + (BM + BN) * 64 + tid * 4) = sr;
+  };
+  const auto store_scales = [&](int64_t step) {
+    *(u32x4*)(lds + 2 * kCodes + ((int)(step - first) >> 1 & 1) * kScales + tid * 16) = scales;
   };
 
   f32x16 acc[TM][TN];
@@ -110,57 +125,77 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_mma_kernel(Args a, uint32
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.f;
 
-  if (first < last) {
-    load(first);
-    store(0);
-  }
-  __syncthreads();
-  for (int64_t step = first; step < last; ++step) {
-    const int buffer = (int)(step - first) & 1;
-    const bool more = step + 1 < last;
-    if (more) load(step + 1);
-    const char* const s = lds + buffer * kStage;
-    int ws[TM], xs[TN];
+  // One step; U: whether it is the second of a pair.
+  const auto products = [&](int64_t step, auto second) {
+    constexpr int U = decltype(second)::value;
+    const char* const c = lds + ((int)(step - first) & 1) * kCodes;
+    const char* const s = lds + 2 * kCodes + ((int)(step - first) >> 1 & 1) * kScales + 8 * U;
+    int ws[TM][2], xs[TN][2];
 #pragma unroll
-    for (int m = 0; m < TM; ++m)
-      ws[m] = *(const int*)(s + (BM + BN) * 64 + ((wm * TM + m) * 32 + lane % 32) * 4) >> (8 * half);
+    for (int m = 0; m < TM; ++m) {
+      const uint2 v = *(const uint2*)(s + ((wm * TM + m) * 32 + lane % 32) * 16);
+      ws[m][0] = (int)(v.x >> (8 * half)), ws[m][1] = (int)(v.y >> (8 * half));
+    }
 #pragma unroll
-    for (int n = 0; n < TN; ++n)
-      xs[n] = *(const int*)(s + (BM + BN) * 64 + (BM + (wn * TN + n) * 32 + lane % 32) * 4) >>
-              (8 * half);
+    for (int n = 0; n < TN; ++n) {
+      const uint2 v = *(const uint2*)(s + (BM + (wn * TN + n) * 32 + lane % 32) * 16);
+      xs[n][0] = (int)(v.x >> (8 * half)), xs[n][1] = (int)(v.y >> (8 * half));
+    }
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-      uint4 wf[TM], xf[TN];
+    for (int sub = 0; sub < 4; ++sub) {
+      u32x4 wf[TM], xf[TN];
 #pragma unroll
-      for (int m = 0; m < TM; ++m) {
-        const int r = (wm * TM + m) * 32 + lane % 32;
-        wf[m] = *(const uint4*)(s + r * 64 + 16 * ((2 * sub + half) ^ ((r >> 2) & 3)));
-      }
+      for (int m = 0; m < TM; ++m) wf[m] = *(const u32x4*)(c + (wread[m] ^ (32 * sub)));
 #pragma unroll
-      for (int n = 0; n < TN; ++n) {
-        const int r = BM + (wn * TN + n) * 32 + lane % 32;
-        xf[n] = *(const uint4*)(s + r * 64 + 16 * ((2 * sub + half) ^ ((r >> 2) & 3)));
-      }
+      for (int n = 0; n < TN; ++n) xf[n] = *(const u32x4*)(c + (xread[n] ^ (32 * sub)));
 #pragma unroll
       for (int n = 0; n < TN; ++n)
 #pragma unroll
         for (int m = 0; m < TM; ++m)
-          acc[m][n] = sub == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                     operand(xf[n]), operand(wf[m]), acc[m][n], 4, 4, 0, xs[n], 0,
-                                     ws[m])
-                               : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                                     operand(xf[n]), operand(wf[m]), acc[m][n], 4, 4, 2, xs[n], 2,
-                                     ws[m]);
+          acc[m][n] = sub % 2 == 0
+                          ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                operand(xf[n]), operand(wf[m]), acc[m][n], 4, 4, 0, xs[n][sub / 2],
+                                0, ws[m][sub / 2])
+                          : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                operand(xf[n]), operand(wf[m]), acc[m][n], 4, 4, 2, xs[n][sub / 2],
+                                2, ws[m][sub / 2]);
     }
-    if (more) store(buffer ^ 1);
+  };
+
+  // A step is made while the next one's loads come; loads past the last step are not
+  // used.  (The scheduling barriers keep the loads before the products: below them they
+  // would be waited for.)
+  if (first < last) {
+    load(first);
+    load_scales(first);
+    store(first);
+    store_scales(first);
+  }
+  __syncthreads();
+  for (int64_t step = first; step < last; step += 2) {
+    load(step + 1);
+    if (step + 2 < last) load_scales(step + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    products(step, std::integral_constant<int, 0>());
+    store(step + 1);
+    __syncthreads();
+    load(step + 2);
+    __builtin_amdgcn_sched_barrier(0);
+    if (step + 1 < last) products(step + 1, std::integral_constant<int, 1>());
+    store(step + 2);
+    store_scales(step + 2);
     __syncthreads();
   }
+  // (every wave is past the last step's barrier)
+  char* const mine = lds + wave * kWriteBytes;
 #pragma unroll
-  for (int m = 0; m < TM; ++m)
-#pragma unroll
-    for (int n = 0; n < TN; ++n)
-      mx4_write<T>(acc[m][n], m0 + (wm * TM + m) * 32, t0 + (wn * TN + n) * 32, a.W.rows, a.X.rows,
-                   a.out, a.ldo, a.part, piece);
+  for (int m = 0; m < TM; ++m) {
+    const int64_t r0 = m0 + (wm * TM + m) * 32, tw = t0 + wn * TN * 32;
+    if (a.part)
+      mx4_write(acc[m], mine, r0, tw, a.W.rows, a.X.rows, a.part + (int64_t)piece * a.W.rows * a.X.rows, a.X.rows);
+    else
+      mx4_write(acc[m], mine, r0, tw, a.W.rows, a.X.rows, (T*)a.out, a.ldo);
+  }
 }
 
 struct Cut {
@@ -169,7 +204,7 @@ struct Cut {
   int32_t pieces, steps;
 };
 // Large tiles where they fill half of the GPU; small ones cut along the inner size
-// until they fill it too, in pieces of at least four steps.
+// until they fill it too, in pieces of at least two steps.
 Cut cut(const Mx4& W, int64_t T) {
   const int64_t steps = cdiv(W.cols, kStep);
   Cut c;
@@ -178,7 +213,7 @@ Cut cut(const Mx4& W, int64_t T) {
   c.tiles_m = (uint32_t)cdiv(W.rows, side);
   c.tiles_n = (uint32_t)cdiv(T, side);
   const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
-  int64_t pieces = c.large || tiles >= 256 ? 1 : std::min<int64_t>(512 / tiles, steps / 4);
+  int64_t pieces = c.large || tiles >= 256 ? 1 : std::min<int64_t>(256 / tiles, steps / 2);
   pieces = std::max<int64_t>(pieces, 1);
   c.steps = (int32_t)cdiv(steps, pieces);
   c.pieces = (int32_t)cdiv(steps, c.steps);
