@@ -62,6 +62,16 @@ __device__ __forceinline__ float hi_f32(uint32_t w, bf16_t*) {
   return __uint_as_float(w & 0xffff0000u);
 }
 
+// Two f32 as a pair of 16 bits, rounded to nearest even (one instruction for bf16).
+__device__ __forceinline__ uint32_t pair16(float lo, float hi, bf16_t*) {
+  typedef __bf16 pair __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, (pair){(__bf16)lo, (__bf16)hi});
+}
+__device__ __forceinline__ uint32_t pair16(float lo, float hi, _Float16*) {
+  typedef _Float16 pair __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, (pair){(_Float16)lo, (_Float16)hi});
+}
+
 template <typename T>
 __device__ __forceinline__ uint16_t bits16(T x) {
   return __builtin_bit_cast(uint16_t, x);

@@ -18,6 +18,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int64_t kMostItems = (int64_t)1 << 31;  // threads of a launch (under 2^32)
 
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
 struct Four {
   uint32_t v[4];
 };
@@ -40,37 +42,54 @@ __device__ __forceinline__ Four philox7(uint32_t c0, uint32_t c1, uint32_t c2, u
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void dropout_kernel(DropoutArgs a) {
-  const int64_t groups = (a.cols + 7) / 8;
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  int64_t r = id / groups;
-  const int64_t g = id - r * groups;
-  r += a.row0;
+  const uint32_t groups = (uint32_t)((a.cols + 7) / 8), id = blockIdx.x * kThreads + threadIdx.x;
+  const uint32_t row = id / groups, g = id - row * groups;
+  const int64_t r = a.row0 + row;
   if (r >= a.rows) return;
   const uint64_t seed = a.state ? a.state[0] : a.seed, step = a.state ? a.state[1] : a.step;
   const Four f = philox7((uint32_t)g, (uint32_t)r, (uint32_t)step, (uint32_t)(step >> 32),
                          (uint32_t)seed, (uint32_t)(seed >> 32));
-  const T* p = (const T*)a.x + r * a.ldx + 8 * g;
-  T* q = (T*)a.out + r * a.ldo + 8 * g;
-  const bool whole = 8 * g + 8 <= a.cols;
-  T t[8];
+  const T* p = (const T*)a.x + r * a.ldx + 8 * (int64_t)g;
+  T* q = (T*)a.out + r * a.ldo + 8 * (int64_t)g;
+  const int64_t c = 8 * (int64_t)g;
+  const bool whole = c + 8 <= a.cols;
+  union {
+    T t[8];
+    uint32_t w[2 * sizeof(T)];
+  } v;
   if (whole) {
-    __builtin_memcpy(t, p, sizeof(t));
+    __builtin_memcpy(v.t, p, sizeof(v.t));
+  } else {
+#pragma unroll
+    for (int i = 0; i < (int)(2 * sizeof(T)); ++i) v.w[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < a.cols) v.t[i] = p[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // all ones where a half is kept: max(half, limit) is the half itself
+    const u16x2 half = __builtin_bit_cast(u16x2, f.v[i]);
+    const u16x2 drop = __builtin_elementwise_max(half, (u16x2)(uint16_t)a.limit) ^ half;
+    uint32_t keep = __builtin_bit_cast(
+        uint32_t, (u16x2)(__builtin_elementwise_min(drop, (u16x2)(uint16_t)1) - (uint16_t)1));
+    if (a.limit > 65535u) keep = 0u;
+    if constexpr (sizeof(T) == 2) {
+      T* const t = nullptr;
+      v.w[i] = pair16(lo_f32(v.w[i], t) * a.scale, hi_f32(v.w[i], t) * a.scale, t) & keep;
+    } else {
+      v.w[2 * i] = __float_as_uint(__uint_as_float(v.w[2 * i]) * a.scale) &
+                   (uint32_t)((int32_t)(keep << 16) >> 16);
+      v.w[2 * i + 1] = __float_as_uint(__uint_as_float(v.w[2 * i + 1]) * a.scale) &
+                       (uint32_t)((int32_t)keep >> 16);
+    }
+  }
+  if (whole) {
+    __builtin_memcpy(q, v.t, sizeof(v.t));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (8 * g + i < a.cols) t[i] = p[i];
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t bits = (f.v[i / 2] >> (16 * (i % 2))) & 0xffffu;
-    t[i] = bits >= a.limit ? from_f32<T>(to_f32(t[i]) * a.scale) : from_f32<T>(0.f);
-  }
-  if (whole) {
-    __builtin_memcpy(q, t, sizeof(t));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (8 * g + i < a.cols) q[i] = t[i];
+      if (c + i < a.cols) q[i] = v.t[i];
   }
 }
 

@@ -185,9 +185,15 @@ __device__ __forceinline__ void mx4_write(const f32x16 (&acc)[TN], char* lds, in
     for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        E v[4];
+        uint32_t v[sizeof(E)];
+        if constexpr (sizeof(E) == 2) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = from_f32<E>(acc[n0 + n][4 * g + i]);
+          for (int i = 0; i < 2; ++i)
+            v[i] = pair16(acc[n0 + n][4 * g + 2 * i], acc[n0 + n][4 * g + 2 * i + 1], (E*)nullptr);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(acc[n0 + n][4 * g + i]);
+        }
         char* const to = lds + lane % 32 * kRow + (32 * n + 8 * g + 4 * (lane / 32)) * sizeof(E);
         __builtin_memcpy(__builtin_assume_aligned(to, 4 * sizeof(E)), v, sizeof(v));
       }

@@ -18,8 +18,8 @@ __global__ __launch_bounds__(kThreads) void mx4_quantize_rows(const T* w, int64_
                                                               int64_t cols, int64_t ld,
                                                               uint32_t* codes, uint8_t* scales) {
   const int64_t nb = (cols + kMx4Block - 1) / kMx4Block;
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t r = id / (4 * nb), word = id - r * 4 * nb;
+  const uint32_t words = 4 * (uint32_t)nb, id = blockIdx.x * kThreads + threadIdx.x;
+  const uint32_t r = id / words, word = id - r * words;
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.f;
@@ -43,37 +43,83 @@ __global__ __launch_bounds__(kThreads) void mx4_quantize_rows(const T* w, int64_
   top = max(top, (uint32_t)__shfl_xor((int)top, 2, 64));
   const uint32_t s = mx4_scale_byte(top);
   if (r >= rows) return;
-  codes[r * 4 * nb + word] = s == 255u ? 0u : mx4_encode(v, mx4_scale(s));
-  if ((word & 3) == 0) scales[r * nb + word / 4] = (uint8_t)s;
+  codes[id] = s == 255u ? 0u : mx4_encode(v, mx4_scale(s));
+  if ((word & 3) == 0) scales[id / 4] = (uint8_t)s;
 }
 
 // Columns of unit stride (activations of features x tokens, quantised as tokens x
-// features): one thread a block, neighbouring threads in neighbouring rows.
+// features): 128 rows (tokens) x 8 blocks a workgroup, a wave a block.  A lane holds the
+// 32 elements of two neighbouring rows, so that a load of the wave is 256 neighbouring
+// bytes and a block's maximum needs no other lane; codes go through shared memory, so
+// that a row's eight blocks are stored as one line.
+constexpr int kTileRows = 128, kTileBlocks = 8;
 template <typename T>
-__global__ __launch_bounds__(kThreads) void mx4_quantize_columns(const T* w, int64_t rows,
-                                                                 int64_t cols, int64_t ld,
-                                                                 uint32_t* codes,
-                                                                 uint8_t* scales) {
+__global__ __launch_bounds__(64 * kTileBlocks) void mx4_quantize_columns(const T* w, int64_t rows,
+                                                                         int64_t cols, int64_t ld,
+                                                                         uint32_t tiles,
+                                                                         uint8_t* codes,
+                                                                         uint8_t* scales) {
+  // a row's codes, and 16 bytes so that neighbouring rows begin in other banks
+  constexpr int kRow = 16 * kTileBlocks + 16;
+  __shared__ __attribute__((aligned(16))) char lds[kTileRows * kRow];
+  __shared__ __attribute__((aligned(8))) uint8_t bytes[kTileRows * kTileBlocks];
   const int64_t nb = (cols + kMx4Block - 1) / kMx4Block;
-  const int64_t r = (int64_t)(blockIdx.x / nb) * kThreads + threadIdx.x, b = blockIdx.x % nb;
-  if (r >= rows) return;
-  const int64_t k0 = b * kMx4Block;
-  float v[4][8];
-  uint32_t top = 0;
+  const int64_t r0 = (int64_t)(blockIdx.x / tiles) * kTileRows;
+  const int64_t b0 = (int64_t)(blockIdx.x % tiles) * kTileBlocks;
+  const int tid = threadIdx.x, lane = tid % 64, wave = wave_uniform(tid / 64);
+  const int64_t r = r0 + 2 * lane, k0 = (b0 + wave) * kMx4Block;
+  if (k0 < cols) {
+    struct Pair {
+      T v[2];
+    } p[kMx4Block];
+    const int n = (int)min((int64_t)kMx4Block, cols - k0);
+    const T* const from = w + k0 * ld + r;
+    if (n == kMx4Block && r0 + kTileRows <= rows) {
 #pragma unroll
-  for (int i = 0; i < kMx4Block; ++i) {
-    v[i / 8][i % 8] = k0 + i < cols ? to_f32(w[(k0 + i) * ld + r]) : 0.f;
-    top = max(top, magnitude(v[i / 8][i % 8]));
+      for (int i = 0; i < kMx4Block; ++i) __builtin_memcpy(&p[i], from + i * ld, sizeof(Pair));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kMx4Block; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          p[i].v[j] = i < n && r + j < rows ? from[i * ld + j] : from_f32<T>(0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kMx4Block; ++i) top = max(top, magnitude(to_f32(p[i].v[j])));
+      const uint32_t s = mx4_scale_byte(top);
+      uint32_t q[4] = {0u, 0u, 0u, 0u};
+      if (s != 255u) {
+        const float scale = mx4_scale(s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = to_f32(p[8 * i + e].v[j]);
+          q[i] = mx4_encode(v, scale);
+        }
+      }
+      *(uint4*)(lds + (2 * lane + j) * kRow + 16 * wave) = make_uint4(q[0], q[1], q[2], q[3]);
+      bytes[(2 * lane + j) * kTileBlocks + wave] = (uint8_t)s;
+    }
   }
-  const uint32_t s = mx4_scale_byte(top);
-  uint4 q = make_uint4(0u, 0u, 0u, 0u);
-  if (s != 255u) {
-    const float scale = mx4_scale(s);
-    q = make_uint4(mx4_encode(v[0], scale), mx4_encode(v[1], scale), mx4_encode(v[2], scale),
-                   mx4_encode(v[3], scale));
+  __syncthreads();
+  const int64_t blocks = min((int64_t)kTileBlocks, nb - b0);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = (tid + 512 * i) / kTileBlocks, b = tid % kTileBlocks;
+    if (r0 + at < rows && b < blocks)
+      *(uint4*)(codes + ((r0 + at) * nb + b0 + b) * 16) = *(const uint4*)(lds + at * kRow + 16 * b);
   }
-  *(uint4*)(codes + (r * nb + b) * 4) = q;
-  scales[r * nb + b] = (uint8_t)s;
+  if (tid < kTileRows && r0 + tid < rows) {
+    uint8_t* const to = scales + (r0 + tid) * nb + b0;
+    if (blocks == kTileBlocks)
+      __builtin_memcpy(to, bytes + tid * kTileBlocks, kTileBlocks);
+    else
+      for (int b = 0; b < blocks; ++b) to[b] = bytes[tid * kTileBlocks + b];
+  }
 }
 
 template <typename T>
@@ -82,17 +128,20 @@ __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(const uint32_t
                                                                   int64_t rows, int64_t cols,
                                                                   T* out, int64_t ldo) {
   const int64_t nb = (cols + kMx4Block - 1) / kMx4Block;
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t r = id / (4 * nb), word = id - r * 4 * nb;
+  const uint32_t words = 4 * (uint32_t)nb, id = blockIdx.x * kThreads + threadIdx.x;
+  const uint32_t r = id / words, word = id - r * words;
   if (r >= rows || 8 * word >= cols) return;
-  const uint32_t w = codes[r * 4 * nb + word];
-  const float s = mx4_scale(scales[r * nb + word / 4]);
+  const uint32_t w = codes[id];
+  const float s = mx4_scale(scales[id / 4]);
   T t[8];
-  const f32x2 a = mx4_pair_f32<0>(w, s), b = mx4_pair_f32<1>(w, s), c = mx4_pair_f32<2>(w, s),
-              d = mx4_pair_f32<3>(w, s);
-  t[0] = from_f32<T>(a[0]), t[1] = from_f32<T>(a[1]), t[2] = from_f32<T>(b[0]);
-  t[3] = from_f32<T>(b[1]), t[4] = from_f32<T>(c[0]), t[5] = from_f32<T>(c[1]);
-  t[6] = from_f32<T>(d[0]), t[7] = from_f32<T>(d[1]);
+  if constexpr (sizeof(T) == 2) {
+    const uint4 v = mx4_eight<T>(w, s);
+    __builtin_memcpy(t, &v, sizeof(t));
+  } else {
+    const f32x2 v[4] = {mx4_pair_f32<0>(w, s), mx4_pair_f32<1>(w, s), mx4_pair_f32<2>(w, s),
+                        mx4_pair_f32<3>(w, s)};
+    __builtin_memcpy(t, v, sizeof(t));
+  }
   T* p = out + r * ldo + 8 * word;
   if (8 * word + 8 <= cols) {
     __builtin_memcpy(p, t, sizeof(t));
@@ -103,16 +152,37 @@ __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(const uint32_t
   }
 }
 
-// out = the pieces' sums, added in order.
+// out = the pieces' sums, added in order: four tokens of a row a thread, the pieces'
+// loads in flight together.
 template <typename T>
-__global__ __launch_bounds__(256) void mx4_sum_kernel(const float* part, int pieces, int64_t M,
-                                                      int64_t tokens, T* out, int64_t ldo) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= M * tokens) return;
-  float v = 0.f;
-  for (int i = 0; i < pieces; ++i) v += part[i * M * tokens + id];
-  const int64_t r = id / tokens;
-  out[r * ldo + id - r * tokens] = from_f32<T>(v);
+__global__ __launch_bounds__(256) void mx4_sum_kernel(const float* part, int pieces, uint32_t rows,
+                                                      uint32_t tokens, T* out, int64_t ldo) {
+  const uint32_t groups = (tokens + 3) / 4, id = blockIdx.x * 256 + threadIdx.x;
+  const uint32_t r = id / groups, t = 4 * (id - r * groups);
+  if (r >= rows) return;
+  const int64_t each = (int64_t)rows * tokens;
+  const float* p = part + (int64_t)r * tokens + t;
+  T* const q = out + r * ldo + t;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (t + 4 <= tokens) {
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i, p += each) {
+      float w[4];
+      __builtin_memcpy(w, p, 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += w[j];
+    }
+    T w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = from_f32<T>(v[j]);
+    __builtin_memcpy(q, w, sizeof(w));
+  } else {
+    for (uint32_t j = 0; t + j < tokens; ++j) {
+      float w = 0.f;
+      for (int i = 0; i < pieces; ++i) w += p[i * each + j];
+      q[j] = from_f32<T>(w);
+    }
+  }
 }
 
 // Threads of a launch (under 2^32); larger matrices take several.
@@ -122,18 +192,21 @@ template <typename T>
 hipError_t quantize(const void* w, int64_t rows, int64_t cols, int64_t rs, int64_t cs,
                     uint8_t* codes, uint8_t* scales, hipStream_t s) {
   const int64_t nb = cdiv(cols, kMx4Block);
-  const int64_t each = cs == 1 ? 4 * nb : nb;
-  const int64_t most = kMostItems / each / kThreads * kThreads;
+  // rows of a launch
+  const int64_t most = kMostItems / (4 * nb) / kThreads * kThreads;
   for (int64_t r = 0; r < rows; r += most) {
     const int64_t n = std::min(most, rows - r);
     const T* const from = (const T*)w + r * rs;
-    uint32_t* const c = (uint32_t*)(codes + r * nb * 16);
-    if (cs == 1)
-      mx4_quantize_rows<T><<<(uint32_t)cdiv(n * each, kThreads), kThreads, 0, s>>>(
-          from, n, cols, rs, c, scales + r * nb);
-    else
-      mx4_quantize_columns<T><<<(uint32_t)(cdiv(n, kThreads) * nb), kThreads, 0, s>>>(
-          from, n, cols, cs, c, scales + r * nb);
+    uint8_t* const c = codes + r * nb * 16;
+    if (cs == 1) {
+      mx4_quantize_rows<T><<<(uint32_t)cdiv(n * 4 * nb, kThreads), kThreads, 0, s>>>(
+          from, n, cols, rs, (uint32_t*)c, scales + r * nb);
+    } else {
+      const uint32_t tiles = (uint32_t)cdiv(nb, kTileBlocks);
+      mx4_quantize_columns<T>
+          <<<(uint32_t)cdiv(n, kTileRows) * tiles, 64 * kTileBlocks, 0, s>>>(from, n, cols, cs, tiles,
+                                                                            c, scales + r * nb);
+    }
   }
   return hipGetLastError();
 }
@@ -166,13 +239,16 @@ hipError_t launch_mx4_dequantize(const Mx4& W, void* out, int dtype, int64_t ldo
 
 hipError_t launch_mx4_sum(const float* part, int pieces, int64_t M, int64_t tokens, void* out,
                           int dtype, int64_t ldo, hipStream_t s) {
-  const uint32_t blocks = (uint32_t)cdiv(M * tokens, 256);
+  const uint32_t blocks = (uint32_t)cdiv(M * cdiv(tokens, 4), 256);
   if (dtype == kF32)
-    mx4_sum_kernel<<<blocks, 256, 0, s>>>(part, pieces, M, tokens, (float*)out, ldo);
+    mx4_sum_kernel<<<blocks, 256, 0, s>>>(part, pieces, (uint32_t)M, (uint32_t)tokens,
+                                             (float*)out, ldo);
   else if (dtype == kF16)
-    mx4_sum_kernel<<<blocks, 256, 0, s>>>(part, pieces, M, tokens, (_Float16*)out, ldo);
+    mx4_sum_kernel<<<blocks, 256, 0, s>>>(part, pieces, (uint32_t)M, (uint32_t)tokens,
+                                             (_Float16*)out, ldo);
   else
-    mx4_sum_kernel<<<blocks, 256, 0, s>>>(part, pieces, M, tokens, (bf16_t*)out, ldo);
+    mx4_sum_kernel<<<blocks, 256, 0, s>>>(part, pieces, (uint32_t)M, (uint32_t)tokens,
+                                             (bf16_t*)out, ldo);
   return hipGetLastError();
 }
 
