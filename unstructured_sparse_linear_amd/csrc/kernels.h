@@ -467,8 +467,7 @@ struct Mx4MatmulArgs {
   const void* x;           // [W.cols][T], transposed [W.rows][T]
   void* out;               // [W.rows][T], transposed [W.cols][T]
   int64_t T, ldx, ldo;
-  float* part;             // sums of the pieces of the inner size, [pieces][rows out][T]
-  int32_t pieces, steps;   // pieces, and steps of 64 in each
+  float* part;             // workspace
 };
 // The product of few tokens (mx4_few.hip), not transposed; no workspace.  128 rows of x
 // are counted in 32 bits.

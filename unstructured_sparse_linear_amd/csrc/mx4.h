@@ -155,6 +155,49 @@ __device__ __forceinline__ uint32_t xcd_index(uint32_t b, uint32_t n) {
   return q * each + min(q, more) + b / 8;
 }
 
+// What a workgroup makes: whole tiles first, then the rest of them in pieces of the
+// inner size.  Tiles go four columns at a time, so that an XCD's workgroups share rows
+// and columns.
+struct Mx4Cut {
+  uint32_t tiles_m, tiles_n;
+  uint32_t whole;          // tiles made whole (a multiple of 8, or all)
+  uint32_t pieces;         // of each of the others
+  int32_t steps;           // in a piece
+};
+struct Mx4Place {
+  uint32_t m, n;           // tile
+  uint32_t rest, piece;    // of the tiles in pieces, which
+  bool cut;
+};
+__host__ __device__ inline void mx4_place(const Mx4Cut& c, uint32_t tile, uint32_t& m,
+                                          uint32_t& n) {
+  const uint32_t band = tile / (4 * c.tiles_m), in = tile % (4 * c.tiles_m);
+  const uint32_t left = c.tiles_n - 4 * band, wide = left < 4 ? left : 4;
+  m = in / wide;
+  n = 4 * band + in % wide;
+}
+__device__ __forceinline__ Mx4Place mx4_place(const Mx4Cut& c, uint32_t block) {
+  Mx4Place p{0, 0, 0, 0, block >= c.whole};
+  uint32_t tile;
+  if (!p.cut) {
+    tile = xcd_index(block, c.whole);
+  } else {
+    const uint32_t rest = c.tiles_m * c.tiles_n - c.whole;
+    const uint32_t i = xcd_index(block - c.whole, rest * c.pieces);
+    p.rest = i % rest;
+    p.piece = i / rest;
+    tile = c.whole + p.rest;
+  }
+  mx4_place(c, tile, p.m, p.n);
+  return p;
+}
+inline uint32_t mx4_blocks(const Mx4Cut& c) {
+  return c.whole + (c.tiles_m * c.tiles_n - c.whole) * c.pieces;
+}
+inline size_t mx4_part_bytes(const Mx4Cut& c, int64_t bm, int64_t bn) {
+  return (size_t)(c.tiles_m * c.tiles_n - c.whole) * c.pieces * bm * bn * 4;
+}
+
 // A wave's memory is written before it is read by other lanes, and read before it is
 // written again.
 __device__ __forceinline__ void wave_fence() {
@@ -218,8 +261,9 @@ __device__ __forceinline__ void mx4_write(const f32x16 (&acc)[TN], char* lds, in
   }
 }
 
-// out = the sums of the pieces, added in order (mx4.hip).
-hipError_t launch_mx4_sum(const float* part, int pieces, int64_t M, int64_t tokens, void* out,
-                          int dtype, int64_t ldo, hipStream_t s);
+// out = the sums of the pieces of the tiles that were cut (bm rows x bn tokens each),
+// added in order (mx4.hip); part is [piece][tile][bm][bn].
+hipError_t launch_mx4_sum(const float* part, const Mx4Cut& c, int bm, int bn, int64_t M,
+                          int64_t tokens, void* out, int dtype, int64_t ldo, hipStream_t s);
 
 }  // namespace spops

@@ -155,33 +155,32 @@ __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(const uint32_t
 // out = the pieces' sums, added in order: four tokens of a row a thread, the pieces'
 // loads in flight together.
 template <typename T>
-__global__ __launch_bounds__(256) void mx4_sum_kernel(const float* part, int pieces, uint32_t rows,
-                                                      uint32_t tokens, T* out, int64_t ldo) {
-  const uint32_t groups = (tokens + 3) / 4, id = blockIdx.x * 256 + threadIdx.x;
-  const uint32_t r = id / groups, t = 4 * (id - r * groups);
-  if (r >= rows) return;
-  const int64_t each = (int64_t)rows * tokens;
-  const float* p = part + (int64_t)r * tokens + t;
-  T* const q = out + r * ldo + t;
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
-  if (t + 4 <= tokens) {
+__global__ __launch_bounds__(256) void mx4_sum_kernel(const float* part, Mx4Cut c, int bm, int bn,
+                                                      int64_t rows, int64_t tokens, T* out,
+                                                      int64_t ldo) {
+  const uint32_t rest = c.tiles_m * c.tiles_n - c.whole, blocks = bm * bn / 1024;
+  const uint32_t tile = blockIdx.x / blocks, at = (blockIdx.x % blocks * 256 + threadIdx.x) * 4;
+  uint32_t m, n;
+  mx4_place(c, c.whole + tile, m, n);
+  const int64_t r = (int64_t)m * bm + at / bn, t = (int64_t)n * bn + at % bn;
+  if (r >= rows || t >= tokens) return;
+  const int64_t each = (int64_t)rest * bm * bn;
+  const float* p = part + (int64_t)tile * bm * bn + at;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int i = 0; i < pieces; ++i, p += each) {
-      float w[4];
-      __builtin_memcpy(w, p, 16);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += w[j];
-    }
-    T w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = from_f32<T>(v[j]);
+  for (uint32_t i = 0; i < c.pieces; ++i, p += each) {
+    // (tokens past the last were not written, and are not written here)
+    const float4 w = *(const float4*)p;
+    v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+  }
+  const T w[4] = {from_f32<T>(v.x), from_f32<T>(v.y), from_f32<T>(v.z), from_f32<T>(v.w)};
+  T* const q = out + r * ldo + t;
+  if (t + 4 <= tokens) {
     __builtin_memcpy(q, w, sizeof(w));
   } else {
-    for (uint32_t j = 0; t + j < tokens; ++j) {
-      float w = 0.f;
-      for (int i = 0; i < pieces; ++i) w += p[i * each + j];
-      q[j] = from_f32<T>(w);
-    }
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (t + j < tokens) q[j] = w[j];
   }
 }
 
@@ -237,18 +236,15 @@ hipError_t launch_mx4_dequantize(const Mx4& W, void* out, int dtype, int64_t ldo
   return dequantize(W, (bf16_t*)out, ldo, s);
 }
 
-hipError_t launch_mx4_sum(const float* part, int pieces, int64_t M, int64_t tokens, void* out,
-                          int dtype, int64_t ldo, hipStream_t s) {
-  const uint32_t blocks = (uint32_t)cdiv(M * cdiv(tokens, 4), 256);
+hipError_t launch_mx4_sum(const float* part, const Mx4Cut& c, int bm, int bn, int64_t M,
+                          int64_t tokens, void* out, int dtype, int64_t ldo, hipStream_t s) {
+  const uint32_t blocks = (c.tiles_m * c.tiles_n - c.whole) * (uint32_t)(bm * bn / 1024);
   if (dtype == kF32)
-    mx4_sum_kernel<<<blocks, 256, 0, s>>>(part, pieces, (uint32_t)M, (uint32_t)tokens,
-                                             (float*)out, ldo);
+    mx4_sum_kernel<<<blocks, 256, 0, s>>>(part, c, bm, bn, M, tokens, (float*)out, ldo);
   else if (dtype == kF16)
-    mx4_sum_kernel<<<blocks, 256, 0, s>>>(part, pieces, (uint32_t)M, (uint32_t)tokens,
-                                             (_Float16*)out, ldo);
+    mx4_sum_kernel<<<blocks, 256, 0, s>>>(part, c, bm, bn, M, tokens, (_Float16*)out, ldo);
   else
-    mx4_sum_kernel<<<blocks, 256, 0, s>>>(part, pieces, (uint32_t)M, (uint32_t)tokens,
-                                             (bf16_t*)out, ldo);
+    mx4_sum_kernel<<<blocks, 256, 0, s>>>(part, c, bm, bn, M, tokens, (bf16_t*)out, ldo);
   return hipGetLastError();
 }
 

@@ -35,10 +35,11 @@ namespace {
 
 constexpr int kStep = 64;
 
-// One tile, and the steps of its inner size.
+// One tile, and the steps of its inner size; part: where the sums of a tile in pieces go.
 struct Tile {
   int64_t m0, t0, first, last;
-  uint32_t piece;
+  float* part;
+  int bn;  // its row
 };
 // F: on f16.  SB: x in a single buffer.
 template <typename T, bool F>
@@ -99,7 +100,9 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
   Raw<T> xr[kPasses];
   // Nothing in a load looks at what another brings, so that they come while the step
   // before is made.  Inside: every load of the step lies inside x (tokens past the last
-  // may hold anything, as their columns are not written).
+  // may hold anything, as their columns are not written).  Rows that start between two
+  // words are loaded as they are: words from the one before on, shifted when they are
+  // stored, took longer (f16, 2011 tokens, 4090 -> 4097: 98.7 us, 91.5 so).
   const auto load_x = [&](int64_t step, auto inside) {
     const int64_t at = step * kStep * a.ldx + t0;
 #pragma unroll
@@ -296,11 +299,11 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
   char* const mine = lds + wave * kWriteBytes;
 #pragma unroll
   for (int m = 0; m < TM; ++m) {
-    const int64_t r0 = m0 + (wm * TM + m) * 32, tw = t0 + wn * TN * 32;
-    if (a.part)
-      mx4_write(acc[m], mine, r0, tw, M, a.T, a.part + (int64_t)tile.piece * M * a.T, a.T);
+    const int64_t r = (wm * TM + m) * 32, t = wn * TN * 32;
+    if (tile.part)
+      mx4_write(acc[m], mine, r, t, M - m0, a.T - t0, tile.part, tile.bn);
     else
-      mx4_write(acc[m], mine, r0, tw, M, a.T, (T*)a.out, a.ldo);
+      mx4_write(acc[m], mine, m0 + r, t0 + t, M, a.T, (T*)a.out, a.ldo);
   }
 }
 
@@ -330,25 +333,21 @@ __device__ __forceinline__ bool wide_scales(const uint8_t* p, int64_t rows, int6
 }
 
 template <typename T, bool TR, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs a,
-                                                                   uint32_t tiles_m,
-                                                                   uint32_t tiles_n) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs a, Mx4Cut c) {
   constexpr bool H = __is_same(T, _Float16);
   __shared__ __attribute__((aligned(16))) char
       lds[std::max(kTileBytes<T, TR, BM, BN, H, false>,
                    H ? kTileBytes<T, TR, BM, 128, false, true> : 0)];
-  const uint32_t index = xcd_index(blockIdx.x, gridDim.x);
-  const uint32_t at = index % (tiles_m * tiles_n), piece = index / (tiles_m * tiles_n);
-  // four columns of tiles at a time, so that an XCD's workgroups share rows and columns
-  const uint32_t band = at / (4 * tiles_m), in = at % (4 * tiles_m);
-  const uint32_t wide = min(4u, tiles_n - 4 * band);
-  const int64_t K = TR ? a.W.rows : a.W.cols;
+  const Mx4Place p = mx4_place(c, blockIdx.x);
+  const int64_t K = TR ? a.W.rows : a.W.cols, steps = (K + kStep - 1) / kStep;
   Tile tile;
-  tile.m0 = (int64_t)(in / wide) * BM;
-  tile.t0 = (int64_t)(4 * band + in % wide) * BN;
-  tile.first = (int64_t)piece * a.steps;
-  tile.last = min(tile.first + a.steps, (K + kStep - 1) / kStep);
-  tile.piece = piece;
+  tile.m0 = (int64_t)p.m * BM;
+  tile.t0 = (int64_t)p.n * BN;
+  tile.first = p.cut ? (int64_t)p.piece * c.steps : 0;
+  tile.last = p.cut ? min(tile.first + c.steps, steps) : steps;
+  const int64_t rest = c.tiles_m * c.tiles_n - c.whole;
+  tile.part = p.cut ? a.part + (p.piece * rest + p.rest) * (BM * BN) : nullptr;
+  tile.bn = BN;
   if constexpr (H) {
     const int64_t nb = (a.W.cols + kMx4Block - 1) / kMx4Block;
     const int64_t r0 = TR ? tile.first * kStep : tile.m0, b0 = TR ? tile.m0 / 32 : 2 * tile.first;
@@ -356,7 +355,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs
     const int64_t n = min(nb - b0, TR ? (int64_t)BM / 32 : 2 * (tile.last - tile.first));
     if (wide_scales<64 * WM * WN>(a.W.scales + r0 * nb + b0, rows, n, nb)) {
       // in two parts x takes twice the room: 128 tokens at a time
-      for (int i = 0; i < BN / 128; ++i, tile.t0 += 128)
+      for (int i = 0; i < BN / 128; ++i, tile.t0 += 128, tile.part += tile.part ? 128 : 0)
         tile_product<T, TR, BM, 128, WM, WN, false, true>(a, tile, lds);
       return;
     }
@@ -364,44 +363,51 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs
   tile_product<T, TR, BM, BN, WM, WN, H, false>(a, tile, lds);
 }
 
-struct Cut {
-  bool large;        // the large tiles
-  uint32_t tiles_m, tiles_n;
-  int32_t pieces, steps;
+constexpr int kSlots = 256;  // compute units
+
+struct Cut : Mx4Cut {
+  bool large;
+  int bm, bn;
 };
 // Large tiles (256 rows; transposed 256 tokens too) where they fill the GPU (4096 x 4096,
-// 2048 tokens: 76 us, 84 with small ones); small ones cut along the inner size until they
-// do, in pieces of at least four steps (4096 x 4096, 512 tokens: 47 us in two pieces, 53
-// in four, 256 tokens 37 in four, 45 in eight: the pieces are written and read again).
+// 2048 tokens: 76 us, 84 with small ones).  Fewer tiles than compute units are cut along
+// the inner size until they do, in pieces of at least four steps (4096 x 4096, 512
+// tokens: 36 us in two pieces, 39 in four, 46 whole: the pieces are written and read
+// again).  Of a few more than a round of them those past it are cut, so that they do not
+// take a round of their own.
 Cut cut(const Mx4& W, int transposed, int dtype, int64_t T) {
   const int64_t M = transposed ? W.cols : W.rows, K = transposed ? W.rows : W.cols;
   const int64_t steps = cdiv(K, kStep);
   Cut c;
   const int64_t wide = transposed ? 256 : 128;
   c.large = dtype != kF32 && cdiv(M, 256) * cdiv(T, wide) >= (transposed ? 128 : 256);
-  c.tiles_m = (uint32_t)cdiv(M, c.large ? 256 : 128);
-  c.tiles_n = (uint32_t)cdiv(T, c.large ? wide : 128);
-  const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
-  const int64_t pieces =
-      c.large ? 1 : std::max<int64_t>(1, std::min<int64_t>(256 / tiles, steps / 4));
-  c.steps = (int32_t)cdiv(steps, pieces);
-  c.pieces = (int32_t)cdiv(steps, c.steps);
+  c.bm = c.large ? 256 : 128;
+  c.bn = c.large ? (int)wide : 128;
+  c.tiles_m = (uint32_t)cdiv(M, c.bm);
+  c.tiles_n = (uint32_t)cdiv(T, c.bn);
+  const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n, rest = tiles % kSlots;
+  // the transposed large tiles have a compute unit each, others share one
+  const int64_t few = tiles < kSlots ? (c.large ? 0 : kSlots) : c.large && transposed ? 128 : 85;
+  const int64_t pieces = rest > 0 && rest <= few ? std::min<int64_t>(kSlots / rest, steps / 4) : 1;
+  c.whole = (uint32_t)(pieces > 1 ? tiles - rest : tiles);
+  c.steps = (int32_t)cdiv(steps, std::max<int64_t>(pieces, 1));
+  c.pieces = (uint32_t)cdiv(steps, c.steps);
   return c;
 }
 
 template <typename T, bool TR>
 void launch(const Mx4MatmulArgs& a, const Cut& c, hipStream_t s) {
-  const uint32_t blocks = c.tiles_m * c.tiles_n * (uint32_t)c.pieces;
+  const uint32_t blocks = mx4_blocks(c);
   if constexpr (sizeof(T) == 2) {
     if (c.large) {
       if constexpr (TR)
-        mx4_tile_kernel<T, TR, 256, 256, 4, 2><<<blocks, 512, 0, s>>>(a, c.tiles_m, c.tiles_n);
+        mx4_tile_kernel<T, TR, 256, 256, 4, 2><<<blocks, 512, 0, s>>>(a, c);
       else
-        mx4_tile_kernel<T, TR, 256, 128, 4, 1><<<blocks, 256, 0, s>>>(a, c.tiles_m, c.tiles_n);
+        mx4_tile_kernel<T, TR, 256, 128, 4, 1><<<blocks, 256, 0, s>>>(a, c);
       return;
     }
   }
-  mx4_tile_kernel<T, TR, 128, 128, 2, 2><<<blocks, 256, 0, s>>>(a, c.tiles_m, c.tiles_n);
+  mx4_tile_kernel<T, TR, 128, 128, 2, 2><<<blocks, 256, 0, s>>>(a, c);
 }
 
 // Up to this many tokens the kernel of few tokens is the faster.
@@ -412,20 +418,15 @@ bool is_few(int transposed, int dtype, int64_t T) {
 template <typename T>
 hipError_t matmul(Mx4MatmulArgs a, int transposed, int dtype, hipStream_t s) {
   Cut c = cut(a.W, transposed, dtype, a.T);
-  if (is_few(transposed, dtype, a.T)) {
-    // rows of x further apart than that kernel counts: no workspace, so in one piece
-    c.pieces = 1;
-    c.steps = INT32_MAX;
-  }
+  // rows of x further apart than the kernel of few tokens counts: no workspace, so whole
+  if (is_few(transposed, dtype, a.T)) c.whole = c.tiles_m * c.tiles_n;
   const int64_t M = transposed ? a.W.cols : a.W.rows;
-  a.pieces = c.pieces;
-  a.steps = c.steps;
-  if (c.pieces == 1) a.part = nullptr;
   if (transposed)
     launch<T, true>(a, c, s);
   else
     launch<T, false>(a, c, s);
-  if (c.pieces > 1) return launch_mx4_sum(a.part, c.pieces, M, a.T, a.out, dtype, a.ldo, s);
+  if (c.whole < c.tiles_m * c.tiles_n)
+    return launch_mx4_sum(a.part, c, c.bm, c.bn, M, a.T, a.out, dtype, a.ldo, s);
   return hipGetLastError();
 }
 
@@ -434,8 +435,7 @@ hipError_t matmul(Mx4MatmulArgs a, int transposed, int dtype, hipStream_t s) {
 size_t mx4_matmul_bytes(const Mx4& W, int transposed, int dtype, int64_t T) {
   if (is_few(transposed, dtype, T)) return 0;
   const Cut c = cut(W, transposed, dtype, T);
-  if (c.pieces == 1) return 0;
-  return (size_t)c.pieces * (size_t)(transposed ? W.cols : W.rows) * (size_t)T * 4;
+  return mx4_part_bytes(c, c.bm, c.bn);
 }
 
 hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, int transposed, int dtype, hipStream_t s) {

@@ -24,7 +24,6 @@ struct Args {
   void* out;
   int64_t ldo;
   float* part;
-  int32_t steps;
 };
 
 __device__ __forceinline__ i32x8 operand(const u32x4& c) {
@@ -34,8 +33,7 @@ __device__ __forceinline__ i32x8 operand(const u32x4& c) {
 
 // BM rows x BN tokens; WM x WN waves.
 template <typename T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void mx4_mma_kernel(Args a, uint32_t tiles_m,
-                                                                  uint32_t tiles_n) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void mx4_mma_kernel(Args a, Mx4Cut cut) {
   constexpr int kThreads = 64 * WM * WN, kRows = BM + BN, kLoads = kRows * kBlocks / kThreads;
   constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
   static_assert(kRows == kThreads && BM % 64 == 0, "a row of scales a thread, waves of one matrix");
@@ -46,13 +44,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_mma_kernel(Args a, uint32
   __shared__ __attribute__((aligned(16))) char lds[2 * (kCodes + kScales)];
 
   const int64_t nb = (a.W.cols + kMx4Block - 1) / kMx4Block;
-  const uint32_t index = xcd_index(blockIdx.x, gridDim.x);
-  const uint32_t tile = index % (tiles_m * tiles_n), piece = index / (tiles_m * tiles_n);
-  const uint32_t band = tile / (4 * tiles_m), in = tile % (4 * tiles_m);
-  const uint32_t wide = min(4u, tiles_n - 4 * band);
-  const int64_t m0 = (int64_t)(in / wide) * BM, t0 = (int64_t)(4 * band + in % wide) * BN;
-  const int64_t first = (int64_t)piece * a.steps;
-  const int64_t last = min(first + a.steps, (nb + kBlocks - 1) / kBlocks);
+  const Mx4Place place = mx4_place(cut, blockIdx.x);
+  const int64_t m0 = (int64_t)place.m * BM, t0 = (int64_t)place.n * BN;
+  const int64_t steps = (nb + kBlocks - 1) / kBlocks;
+  const int64_t first = place.cut ? (int64_t)place.piece * cut.steps : 0;
+  const int64_t last = place.cut ? min(first + cut.steps, steps) : steps;
+  const int64_t rest = cut.tiles_m * cut.tiles_n - cut.whole;
+  float* const part =
+      place.cut ? a.part + (place.piece * rest + place.rest) * (BM * BN) : nullptr;
 
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   const int wm = wave / WN, wn = wave % WN, half = lane / 32;
@@ -164,7 +163,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_mma_kernel(Args a, uint32
 
   // A step is made while the next one's loads come; loads past the last step are not
   // used.  (The scheduling barriers keep the loads before the products: below them they
-  // would be waited for.)
+  // would be waited for.  Loads two steps ahead were no faster.)
   if (first < last) {
     load(first);
     load_scales(first);
@@ -190,47 +189,48 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_mma_kernel(Args a, uint32
   char* const mine = lds + wave * kWriteBytes;
 #pragma unroll
   for (int m = 0; m < TM; ++m) {
-    const int64_t r0 = m0 + (wm * TM + m) * 32, tw = t0 + wn * TN * 32;
-    if (a.part)
-      mx4_write(acc[m], mine, r0, tw, a.W.rows, a.X.rows, a.part + (int64_t)piece * a.W.rows * a.X.rows, a.X.rows);
+    const int64_t r = (wm * TM + m) * 32, t = wn * TN * 32;
+    if (part)
+      mx4_write(acc[m], mine, r, t, a.W.rows - m0, a.X.rows - t0, part, BN);
     else
-      mx4_write(acc[m], mine, r0, tw, a.W.rows, a.X.rows, (T*)a.out, a.ldo);
+      mx4_write(acc[m], mine, m0 + r, t0 + t, a.W.rows, a.X.rows, (T*)a.out, a.ldo);
   }
 }
 
-struct Cut {
-  bool large;
-  uint32_t tiles_m, tiles_n;
-  int32_t pieces, steps;
+struct Cut : Mx4Cut {
+  int side;
 };
-// Large tiles where they fill half of the GPU; few small ones are cut along the inner
-// size, in pieces of at least two steps (4096 x 4096, 64 tokens: 12.6 us in four pieces,
-// 13.9 in eight, 19.8 whole; 512 tokens: 21.3 whole, 27 in two, which are written and
-// read again).
+// Tiles of 256, 128 or 64 square, the largest that fill the GPU (4096 x 4096, 1024
+// tokens: 21.8 us with 128, 24.4 with 64; 512: 18.9 and 17.7, 128: 17.1 and 12.6); few
+// small ones are cut along the inner size, in pieces of at least two steps (64 tokens:
+// 10.2 us in four pieces, 12.8 in eight, which are written and read again).
 Cut cut(const Mx4& W, int64_t T) {
   const int64_t steps = cdiv(W.cols, kStep);
   Cut c;
-  c.large = cdiv(W.rows, 256) * cdiv(T, 256) >= 128;
-  const int64_t side = c.large ? 256 : 128;
-  c.tiles_m = (uint32_t)cdiv(W.rows, side);
-  c.tiles_n = (uint32_t)cdiv(T, side);
+  c.side = 64;
+  if (cdiv(W.rows, 128) * cdiv(T, 128) >= 256) c.side = 128;
+  if (cdiv(W.rows, 256) * cdiv(T, 256) >= 160) c.side = 256;
+  c.tiles_m = (uint32_t)cdiv(W.rows, c.side);
+  c.tiles_n = (uint32_t)cdiv(T, c.side);
   const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
-  int64_t pieces = c.large || tiles >= 128 ? 1 : std::min<int64_t>(128 / tiles, steps / 2);
-  pieces = std::max<int64_t>(pieces, 1);
+  const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(256 / tiles, steps / 2));
+  c.whole = (uint32_t)(pieces > 1 ? 0 : tiles);
   c.steps = (int32_t)cdiv(steps, pieces);
-  c.pieces = (int32_t)cdiv(steps, c.steps);
+  c.pieces = (uint32_t)cdiv(steps, c.steps);
   return c;
 }
 
 template <typename T>
-hipError_t matmul4(Args a, const Cut& c, int dtype, hipStream_t s) {
-  const uint32_t blocks = c.tiles_m * c.tiles_n * (uint32_t)c.pieces;
-  if (c.large)
-    mx4_mma_kernel<T, 256, 256, 4, 2><<<blocks, 512, 0, s>>>(a, c.tiles_m, c.tiles_n);
+hipError_t matmul4(const Args& a, const Cut& c, int dtype, hipStream_t s) {
+  const uint32_t blocks = mx4_blocks(c);
+  if (c.side == 256)
+    mx4_mma_kernel<T, 256, 256, 4, 2><<<blocks, 512, 0, s>>>(a, c);
+  else if (c.side == 128)
+    mx4_mma_kernel<T, 128, 128, 2, 2><<<blocks, 256, 0, s>>>(a, c);
   else
-    mx4_mma_kernel<T, 128, 128, 2, 2><<<blocks, 256, 0, s>>>(a, c.tiles_m, c.tiles_n);
-  if (c.pieces > 1)
-    return launch_mx4_sum(a.part, c.pieces, a.W.rows, a.X.rows, a.out, dtype, a.ldo, s);
+    mx4_mma_kernel<T, 64, 64, 2, 1><<<blocks, 128, 0, s>>>(a, c);
+  if (c.whole < c.tiles_m * c.tiles_n)
+    return launch_mx4_sum(a.part, c, c.side, c.side, a.W.rows, a.X.rows, a.out, dtype, a.ldo, s);
   return hipGetLastError();
 }
 
@@ -238,13 +238,13 @@ hipError_t matmul4(Args a, const Cut& c, int dtype, hipStream_t s) {
 
 size_t mx4_matmul4_bytes(const Mx4& W, int64_t T) {
   const Cut c = cut(W, T);
-  return c.pieces == 1 ? 0 : (size_t)c.pieces * (size_t)W.rows * (size_t)T * 4;
+  return mx4_part_bytes(c, c.side, c.side);
 }
 
 hipError_t launch_mx4_matmul4(const Mx4& W, const Mx4& X, void* out, int dtype, int64_t ldo,
                               void* ws, hipStream_t s) {
   const Cut c = cut(W, X.rows);
-  const Args a{W, X, out, ldo, c.pieces > 1 ? (float*)ws : nullptr, c.steps};
+  const Args a{W, X, out, ldo, (float*)ws};
   if (dtype == kF32) return matmul4<float>(a, c, dtype, s);
   if (dtype == kF16) return matmul4<_Float16>(a, c, dtype, s);
   return matmul4<bf16_t>(a, c, dtype, s);
