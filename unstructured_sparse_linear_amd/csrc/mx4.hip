@@ -159,7 +159,8 @@ __global__ __launch_bounds__(256) void mx4_sum_kernel(const float* part, Mx4Cut 
                                                       int64_t rows, int64_t tokens, T* out,
                                                       int64_t ldo) {
   const uint32_t rest = c.tiles_m * c.tiles_n - c.whole, blocks = bm * bn / 1024;
-  const uint32_t tile = blockIdx.x / blocks, at = (blockIdx.x % blocks * 256 + threadIdx.x) * 4;
+  const uint32_t index = xcd_index(blockIdx.x, gridDim.x);
+  const uint32_t tile = index / blocks, at = (index % blocks * 256 + threadIdx.x) * 4;
   uint32_t m, n;
   mx4_place(c, c.whole + tile, m, n);
   const int64_t r = (int64_t)m * bm + at / bn, t = (int64_t)n * bn + at % bn;

@@ -371,10 +371,11 @@ struct Cut : Mx4Cut {
 };
 // Large tiles (256 rows; transposed 256 tokens too) where they fill the GPU (4096 x 4096,
 // 2048 tokens: 76 us, 84 with small ones).  Fewer tiles than compute units are cut along
-// the inner size until they do, in pieces of at least four steps (4096 x 4096, 512
-// tokens: 36 us in two pieces, 39 in four, 46 whole: the pieces are written and read
-// again).  Of a few more than a round of them those past it are cut, so that they do not
-// take a round of their own.
+// the inner size until they do, in pieces of at least four steps (4096 x 4096, 256
+// tokens: 24.6 us in four pieces, 28.7 in eight, 42 whole: the pieces are written and
+// read again).  Of a few more than a round of them those past it are cut, so that they do
+// not take a round of their own (2304 tokens: 84 us, 103 whole; gradient of 4352 tokens
+// 155 and 215).
 Cut cut(const Mx4& W, int transposed, int dtype, int64_t T) {
   const int64_t M = transposed ? W.cols : W.rows, K = transposed ? W.rows : W.cols;
   const int64_t steps = cdiv(K, kStep);
@@ -410,9 +411,10 @@ void launch(const Mx4MatmulArgs& a, const Cut& c, hipStream_t s) {
   mx4_tile_kernel<T, TR, 128, 128, 2, 2><<<blocks, 256, 0, s>>>(a, c);
 }
 
-// Up to this many tokens the kernel of few tokens is the faster.
+// Up to this many tokens the kernel of few tokens is the faster (bf16 4096 -> 11008, 64
+// tokens: 23.9 us, 30.4 in tiles; 128: 44.6 and 31.7; f32 4096 x 4096, 32: 23.8 and 26.0).
 bool is_few(int transposed, int dtype, int64_t T) {
-  return !transposed && T <= (dtype == kF32 ? 32 : 128);
+  return !transposed && T <= (dtype == kF32 ? 32 : 64);
 }
 
 template <typename T>
