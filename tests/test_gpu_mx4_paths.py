@@ -79,6 +79,21 @@ def test_one_wide_block_in_f16(rows, cols, tokens, transposed, scale):
     assert torch.isinf(got[must]).all()
 
 
+def test_wide_blocks_in_large_tiles():
+    """Every tile of 256 square, whole and in pieces, makes its tokens in two halves, one
+    after the other in the same shared memory."""
+    rows, cols, tokens = 530, 4352, 4090
+    W, _ = whole_matrix(4, rows, cols, low=118, high=121)
+    W.scales[::128, ::4] = 90
+    w = S.mx4_dequantize(W).double().t().contiguous()
+    x = whole_numbers((rows, tokens), "f16", 4)
+    want, size = torch.mm(w, x.double()), torch.mm(w.abs(), x.double().abs())
+    limit = torch.from_numpy(ref.bound(want.cpu().numpy(), rows, size.cpu().numpy(), "f16")).cuda()
+    got = [S.mx4_matmul(W, x, transposed=True) for _ in range(3)]
+    assert ((got[0].double() - want).abs() <= limit).all()
+    assert torch.equal(got[1], got[0]) and torch.equal(got[2], got[0])
+
+
 # tiles of 256, 128 and 64 square, in pieces or whole
 FOUR = [(2570, 300, 4090), (2049, 290, 2049), (2050, 1000, 300), (300, 4097, 70), (70, 8200, 33)]
 

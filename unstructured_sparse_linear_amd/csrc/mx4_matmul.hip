@@ -355,8 +355,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_tile_kernel(Mx4MatmulArgs
     const int64_t n = min(nb - b0, TR ? (int64_t)BM / 32 : 2 * (tile.last - tile.first));
     if (wide_scales<64 * WM * WN>(a.W.scales + r0 * nb + b0, rows, n, nb)) {
       // in two parts x takes twice the room: 128 tokens at a time
-      for (int i = 0; i < BN / 128; ++i, tile.t0 += 128, tile.part += tile.part ? 128 : 0)
+      for (int i = 0; i < BN / 128; ++i, tile.t0 += 128, tile.part += tile.part ? 128 : 0) {
         tile_product<T, TR, BM, 128, WM, WN, false, true>(a, tile, lds);
+        // the output of the last 128 has left shared memory before the next begin
+        __syncthreads();
+      }
       return;
     }
   }
