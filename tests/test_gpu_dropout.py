@@ -156,3 +156,18 @@ def test_more_than_one_launch():
         assert np.array_equal((x[r:r + 4] != 0).cpu().numpy(), want)
     del x
     torch.cuda.empty_cache()
+
+
+def test_every_element_once_over_launches():
+    """In place, with rows whose groups do not fill the last workgroup of a launch: none of
+    the next launch's elements is scaled twice."""
+    cols = 24
+    first = (1 << 31) // 3  # rows of the first launch
+    rows = first + 200
+    x = torch.ones(rows, cols, dtype=torch.bfloat16, device="cuda")
+    S.dropout(x, 0.5, SEED, 5, out=x)
+    want = torch.where(torch.from_numpy(ref.random16(200, cols, SEED, 5, first - 100) >= 32768),
+                       2.0, 0.0)
+    assert torch.equal(x[first - 100:first + 100].float().cpu(), want.float())
+    del x
+    torch.cuda.empty_cache()

@@ -103,9 +103,11 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(DropoutArgs a) {
 
 hipError_t launch_dropout(DropoutArgs a, int dtype, hipStream_t s) {
   const int64_t groups = cdiv(a.cols, 8), most = std::max<int64_t>(1, kMostItems / groups);
-  for (a.row0 = 0; a.row0 < a.rows; a.row0 += most) {
-    const uint32_t blocks =
-        (uint32_t)cdiv(std::min(most, a.rows - a.row0) * groups, kThreads);
+  const int64_t rows = a.rows;
+  for (a.row0 = 0; a.row0 < rows; a.row0 = a.rows) {
+    // the last workgroup reaches past the launch's rows
+    a.rows = std::min(rows, a.row0 + most);
+    const uint32_t blocks = (uint32_t)cdiv((a.rows - a.row0) * groups, kThreads);
     if (dtype == kF32)
       dropout_kernel<float><<<blocks, kThreads, 0, s>>>(a);
     else if (dtype == kF16)

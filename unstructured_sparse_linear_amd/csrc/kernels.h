@@ -486,7 +486,7 @@ struct DropoutArgs {
   const void* x;
   void* out;
   int64_t rows, cols, ldx, ldo;
-  int64_t row0;            // the launch's first row
+  int64_t row0;            // the launch's first row (rows: where its rows end)
   const uint64_t* state;   // seed and step on the device, or null
   uint64_t seed, step;
   uint32_t limit;          // of 65536 elements, those that are dropped
