@@ -532,8 +532,9 @@ spops_status spops_clip_grad_norm(const spops_clip_tensor* tensors, int64_t coun
  * specification 1.0).  With nb = ceil(cols / 32):
  *   codes:  [rows][16 nb], 16-byte aligned; element 2j of a row is the low half of
  *           byte j, element 2j + 1 the high half.  Elements past cols are zero.
- *   scales: [rows][nb]; s stands for 2^(s - 127), 255 makes the block NaN.  (From
- *           253 on a block's elements may pass the range of f32: infinities.)
+ *   scales: [rows][nb]; s stands for 2^(s - 127), 255 makes the block NaN.  (253 and
+ *           254, which quantising never gives, let elements pass the range of f32:
+ *           they are infinities, and in products infinities or NaN.)
  * rows and cols in 1..2^24. */
 typedef struct spops_mx4 {
   int64_t rows, cols;

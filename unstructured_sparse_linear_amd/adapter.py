@@ -230,13 +230,15 @@ class LowRankAdapters(torch.nn.Module):
                                           dropout)
 
     yt may come from any layer on xt, a dense product, a SparseAdapter or an Mx4Linear;
-    W may be an Mx4Matrix.  scale and ranks (one value per adapter, of any device and
+    W may be an Mx4Matrix (whose product is rounded before the adapters' part is added,
+    in two passes).  scale and ranks (one value per adapter, of any device and
     type) are kept as float32 and int32 buffers, also where the module is cast.
 
     With dropout = p, forward in training drops elements of xt on the adapters' side
     (not in yt) with probability p.  The masks follow from `dropout_state`, an int64
     buffer of a seed and a step that each such call advances on the device; seed
-    defaults to a number of torch's generator."""
+    defaults to a number of torch's generator.  A forward pass that is run again (for
+    activations that were not kept) has to start from the same dropout_state."""
 
     def __init__(self, adapters: int, rank: int, in_features: int, out_features: int,
                  scale: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None,

@@ -4,6 +4,12 @@
 // v_mfma_scale_f32_32x32x64 takes both as they are stored: a lane holds one block of
 // one row (row = lane % 32, block = lane / 32) and its scale byte.  Products are
 // exact, the sums f32.
+//
+// A step of 256 k takes whole lines (128 bytes) of each row's codes through shared
+// memory, and scales come for two steps at a time.  8192 tokens, 4096 -> 11008, bf16 out:
+// 290 us, 2.5 PFLOP/s (the matrix cores reach 5.9 on random operands); its steps are so
+// short that barriers and shared memory bound it.  300 tokens, 4096 x 4096: 18 us, bound by
+// the chain of a tile's steps.
 #include <algorithm>
 #include <type_traits>
 
