@@ -59,7 +59,9 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
   // are, 64 bytes of codes and 4 scales a row
   constexpr int kWBytes = TR ? kStep * BM * 2 : BM * 68;
   constexpr int kW = TR ? 1 : BM * 4 / kThreads;  // loads of codes
-  static_assert(!TR || kThreads == kStep * kBlocks, "a block a thread");
+  // transposed, a block a thread, of the first threads
+  constexpr int kLoaders = kStep * kBlocks;
+  static_assert(!TR || kThreads >= kLoaders, "a block a thread");
   static_assert(WM * WN * kWriteBytes <= kTileBytes<T, TR, BM, BN, F, SB>, "room for output");
   static_assert(TR || (BM * 4 % kThreads == 0 && BM <= kThreads), "whole loads");
   using E = std::conditional_t<F, _Float16, bf16_t>;
@@ -145,6 +147,7 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
   const auto load_w = [&](int64_t step, auto inside) {
     constexpr bool I = decltype(inside)::value;
     if constexpr (TR) {
+      if (kThreads > kLoaders && tid >= kLoaders) return;
       const int64_t r = step * kStep + wrow;
       const int64_t at = (I ? r : min(r, W.rows - 1)) * nb + min(m0 / kMx4Block + wblock, nb - 1);
       wr[0] = *(const u32x4*)(W.codes + at * 16);
@@ -177,6 +180,7 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
   const auto store_w = [&](int64_t step) {
     char* const to = wlds + ((int)(step - first) >> (TR ? 0 : 1) & 1) * kWBytes;
     if constexpr (TR) {
+      if (kThreads > kLoaders && tid >= kLoaders) return;
       const float scale = mx4_scale(step * kStep + wrow < W.rows ? ws : 127u);
       const uint32_t words[4] = {wr[0][0], wr[0][1], wr[0][2], wr[0][3]};
 #pragma unroll
@@ -411,7 +415,12 @@ void launch(const Mx4MatmulArgs& a, const Cut& c, hipStream_t s) {
       return;
     }
   }
-  mx4_tile_kernel<T, TR, 128, 128, 2, 2><<<blocks, 256, 0, s>>>(a, c);
+  // f32, whose x takes the whole shared memory in its three parts: eight waves (gradient of
+  // 512 tokens, 2048 x 2048: 31.9 us, 35.7 with four; 2048 tokens, 4096 x 4096: 256, 316)
+  if constexpr (sizeof(T) == 4)
+    mx4_tile_kernel<T, TR, 128, 128, 2, 4><<<blocks, 512, 0, s>>>(a, c);
+  else
+    mx4_tile_kernel<T, TR, 128, 128, 2, 2><<<blocks, 256, 0, s>>>(a, c);
 }
 
 // Up to this many tokens the kernel of few tokens is the faster (bf16 4096 -> 11008, 64

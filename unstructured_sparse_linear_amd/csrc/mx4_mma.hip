@@ -8,8 +8,8 @@
 // A step of 256 k takes whole lines (128 bytes) of each row's codes through shared
 // memory, and scales come for two steps at a time.  8192 tokens, 4096 -> 11008, bf16 out:
 // 290 us, 2.5 PFLOP/s (the matrix cores reach 5.9 on random operands); its steps are so
-// short that barriers and shared memory bound it.  300 tokens, 4096 x 4096: 18 us, bound by
-// the chain of a tile's steps.
+// short that barriers and shared memory bound it.  300 tokens, 4096 x 4096: 15.4 us,
+// bound by the chain of a tile's steps.
 #include <algorithm>
 #include <type_traits>
 
@@ -21,6 +21,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 256;           // k of a step: eight blocks, 128 bytes of a row
 constexpr int kBlocks = kStep / 32;
@@ -37,9 +38,10 @@ __device__ __forceinline__ i32x8 operand(const u32x4& c) {
   return v;
 }
 
-// BM rows x BN tokens; WM x WN waves.
-template <typename T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void mx4_mma_kernel(Args a, Mx4Cut cut) {
+// BM rows x BN tokens; KG groups of WM x WN waves, each with a part of the steps and shared
+// memory of its own.
+template <typename T, int BM, int BN, int WM, int WN, int KG>
+__global__ __launch_bounds__(64 * WM * WN * KG, 2) void mx4_mma_kernel(Args a, Mx4Cut cut) {
   constexpr int kThreads = 64 * WM * WN, kRows = BM + BN, kLoads = kRows * kBlocks / kThreads;
   constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
   static_assert(kRows == kThreads && BM % 64 == 0, "a row of scales a thread, waves of one matrix");
@@ -47,19 +49,25 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_mma_kernel(Args a, Mx4Cut
   static_assert(BM * kBlocks % kThreads == 0 &&
                     WM * WN * kWriteBytes <= 2 * (kCodes + kScales),
                 "whole loads of each matrix, room for the output");
-  __shared__ __attribute__((aligned(16))) char lds[2 * (kCodes + kScales)];
+  constexpr int kGroupBytes = 2 * (kCodes + kScales);
+  static_assert(KG == 1 || BM * BN * 4 <= kGroupBytes, "room for the sums");
+  __shared__ __attribute__((aligned(16))) char all[KG * kGroupBytes];
 
   const int64_t nb = (a.W.cols + kMx4Block - 1) / kMx4Block;
   const Mx4Place place = mx4_place(cut, blockIdx.x);
   const int64_t m0 = (int64_t)place.m * BM, t0 = (int64_t)place.n * BN;
   const int64_t steps = (nb + kBlocks - 1) / kBlocks;
-  const int64_t first = place.cut ? (int64_t)place.piece * cut.steps : 0;
-  const int64_t last = place.cut ? min(first + cut.steps, steps) : steps;
+  const int64_t from = place.cut ? (int64_t)place.piece * cut.steps : 0;
+  const int64_t to = place.cut ? min(from + cut.steps, steps) : steps;
+  const int group = KG == 1 ? 0 : wave_uniform((int)threadIdx.x / kThreads);
+  const int64_t each = KG == 1 ? to - from : (to - from + KG - 1) / KG;
+  const int64_t first = from + group * each, last = min(first + each, to);
+  char* const lds = all + group * kGroupBytes;
   const int64_t rest = cut.tiles_m * cut.tiles_n - cut.whole;
   float* const part =
       place.cut ? a.part + (place.piece * rest + place.rest) * (BM * BN) : nullptr;
 
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int tid = (int)threadIdx.x % kThreads, lane = tid % 64, wave = tid / 64;
   const int wm = wave / WN, wn = wave % WN, half = lane / 32;
   // a row's eight blocks are turned by the row, so that 16 rows read at once lie in
   // different banks
@@ -177,11 +185,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_mma_kernel(Args a, Mx4Cut
     store_scales(first);
   }
   __syncthreads();
-  for (int64_t step = first; step < last; step += 2) {
+  for (int64_t step = first; step < first + each; step += 2) {
     load(step + 1);
     if (step + 2 < last) load_scales(step + 2);
     __builtin_amdgcn_sched_barrier(0);
-    products(step, std::integral_constant<int, 0>());
+    if (KG == 1 || step < last) products(step, std::integral_constant<int, 0>());
     store(step + 1);
     __syncthreads();
     load(step + 2);
@@ -192,6 +200,36 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_mma_kernel(Args a, Mx4Cut
     __syncthreads();
   }
   // (every wave is past the last step's barrier)
+  if constexpr (KG > 1) {
+    const auto at = [&](int g, int m, int n, int i) {
+      return (f32x4*)(all + g * kGroupBytes) +
+             (((m * TN + n) * 4 + i) * WM * WN + wave) * 64 + lane;
+    };
+    if (group > 0) {
+#pragma unroll
+      for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int n = 0; n < TN; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *at(group, m, n, i) = (f32x4){acc[m][n][4 * i], acc[m][n][4 * i + 1],
+                                          acc[m][n][4 * i + 2], acc[m][n][4 * i + 3]};
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < KG; ++g)
+#pragma unroll
+      for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int n = 0; n < TN; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x4 v = *at(g, m, n, i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[m][n][4 * i + j] += v[j];
+          }
+  }
   char* const mine = lds + wave * kWriteBytes;
 #pragma unroll
   for (int m = 0; m < TM; ++m) {
@@ -208,8 +246,8 @@ struct Cut : Mx4Cut {
 };
 // Tiles of 256, 128 or 64 square, the largest that fill the GPU (4096 x 4096, 1024
 // tokens: 21.8 us with 128, 24.4 with 64; 512: 18.9 and 17.7, 128: 17.1 and 12.6); few
-// small ones are cut along the inner size, in pieces of at least two steps (64 tokens:
-// 10.2 us in four pieces, 12.8 in eight, which are written and read again).
+// small ones are cut along the inner size, in pieces of at least four steps, which two
+// groups of waves make (64 tokens: 9.2 us, 10.3 in pieces for four groups).
 Cut cut(const Mx4& W, int64_t T) {
   const int64_t steps = cdiv(W.cols, kStep);
   Cut c;
@@ -219,7 +257,7 @@ Cut cut(const Mx4& W, int64_t T) {
   c.tiles_m = (uint32_t)cdiv(W.rows, c.side);
   c.tiles_n = (uint32_t)cdiv(T, c.side);
   const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n;
-  const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(256 / tiles, steps / 2));
+  const int64_t pieces = std::max<int64_t>(1, std::min<int64_t>(256 / tiles, steps / 4));
   c.whole = (uint32_t)(pieces > 1 ? 0 : tiles);
   c.steps = (int32_t)cdiv(steps, pieces);
   c.pieces = (uint32_t)cdiv(steps, c.steps);
@@ -230,11 +268,16 @@ template <typename T>
 hipError_t matmul4(const Args& a, const Cut& c, int dtype, hipStream_t s) {
   const uint32_t blocks = mx4_blocks(c);
   if (c.side == 256)
-    mx4_mma_kernel<T, 256, 256, 4, 2><<<blocks, 512, 0, s>>>(a, c);
+    mx4_mma_kernel<T, 256, 256, 4, 2, 1><<<blocks, 512, 0, s>>>(a, c);
   else if (c.side == 128)
-    mx4_mma_kernel<T, 128, 128, 2, 2><<<blocks, 256, 0, s>>>(a, c);
+    mx4_mma_kernel<T, 128, 128, 2, 2, 1><<<blocks, 256, 0, s>>>(a, c);
+  else if (c.steps >= 4)
+    // two waves a tile leave its steps one after the other: two groups of them 15.4 us for
+    // 300 tokens, 4096 x 4096, one 18.4, four (a workgroup a compute unit) 21.1; of 512 x
+    // 512 x 512, two steps, one 4.4 us, two 5.9
+    mx4_mma_kernel<T, 64, 64, 2, 1, 2><<<blocks, 256, 0, s>>>(a, c);
   else
-    mx4_mma_kernel<T, 64, 64, 2, 1><<<blocks, 128, 0, s>>>(a, c);
+    mx4_mma_kernel<T, 64, 64, 2, 1, 1><<<blocks, 128, 0, s>>>(a, c);
   if (c.whole < c.tiles_m * c.tiles_n)
     return launch_mx4_sum(a.part, c, c.side, c.side, a.W.rows, a.X.rows, a.out, dtype, a.ldo, s);
   return hipGetLastError();
