@@ -99,21 +99,25 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
   const T* const x = (const T*)a.x;
   const int64_t end = (K - 1) * a.ldx + a.T;  // of x
   const int64_t xlane = xrow * a.ldx + 8 * xchunk;
-  Raw<T> xr[kPasses];
+  // transposed, small tiles of 16 bits load two steps ahead (gradient of 1024 tokens,
+  // 4096 x 4096: 49.4 us, 55.1 one ahead; no faster where W comes for two steps anyhow,
+  // nor on large tiles)
+  constexpr bool kTwo = TR && BM == 128 && sizeof(T) == 2 && !SB;
+  Raw<T> xr[1 + kTwo][kPasses];
   // Nothing in a load looks at what another brings, so that they come while the step
   // before is made.  Inside: every load of the step lies inside x (tokens past the last
   // may hold anything, as their columns are not written).  Rows that start between two
   // words are loaded as they are: words from the one before on, shifted when they are
   // stored, took longer (f16, 2011 tokens, 4090 -> 4097: 98.7 us, 91.5 so).
-  const auto load_x = [&](int64_t step, auto inside) {
+  const auto load_x = [&](int64_t step, auto inside, int to = 0) {
     const int64_t at = step * kStep * a.ldx + t0;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       if constexpr (decltype(inside)::value) {
-        __builtin_memcpy(&xr[i], x + at + i * kRows * a.ldx + xlane, sizeof(xr[i]));
+        __builtin_memcpy(&xr[to][i], x + at + i * kRows * a.ldx + xlane, sizeof(xr[to][i]));
       } else {
         const int64_t k = step * kStep + i * kRows + xrow, t = t0 + 8 * xchunk;
-        xr[i] = load_until(x, k * a.ldx + t, k < K && t < a.T ? end : 0);
+        xr[to][i] = load_until(x, k * a.ldx + t, k < K && t < a.T ? end : 0);
       }
     }
   };
@@ -126,12 +130,12 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
     else
       load_x(step, std::false_type());
   };
-  const auto store_x = [&](int64_t step) {
+  const auto store_x = [&](int64_t step, int from = 0) {
     char* const xs = lds + (SB ? 0 : (int)(step - first) & 1) * P * kXBytes;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       uint4 part[P];
-      split<T, P>(xr[i], part);
+      split<T, P>(xr[from][i], part);
 #pragma unroll
       for (int p = 0; p < P; ++p)
         *(uint4*)(xs + p * kXBytes + xstore + i * kRows * kChunks * 16) = part[p];
@@ -142,34 +146,34 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
   // again: what they give meets zeros of x, for which scales past the inner size are
   // made finite, or is not written.
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  u32x4 wr[kW];
-  uint32_t ws = 0;
-  const auto load_w = [&](int64_t step, auto inside) {
+  u32x4 wr[1 + kTwo][kW];
+  uint32_t ws[1 + kTwo] = {};
+  const auto load_w = [&](int64_t step, auto inside, int into = 0) {
     constexpr bool I = decltype(inside)::value;
     if constexpr (TR) {
       if (kThreads > kLoaders && tid >= kLoaders) return;
       const int64_t r = step * kStep + wrow;
       const int64_t at = (I ? r : min(r, W.rows - 1)) * nb + min(m0 / kMx4Block + wblock, nb - 1);
-      wr[0] = *(const u32x4*)(W.codes + at * 16);
-      ws = W.scales[at];
+      wr[into][0] = *(const u32x4*)(W.codes + at * 16);
+      ws[into] = W.scales[at];
     } else {
 #pragma unroll
       for (int i = 0; i < kW; ++i) {
         const int id = tid + i * kThreads;
         const int64_t r = min(m0 + id / 4, W.rows - 1), b = 2 * step + id % 4;
-        wr[i] = *(const u32x4*)(W.codes + (r * nb + (I ? b : min(b, nb - 1))) * 16);
+        wr[into][i] = *(const u32x4*)(W.codes + (r * nb + (I ? b : min(b, nb - 1))) * 16);
       }
       if (BM == kThreads || tid < BM) {
         const uint8_t* const p = W.scales + min(m0 + tid, W.rows - 1) * nb + 2 * step;
         if constexpr (I) {
           typedef uint32_t word __attribute__((aligned(1)));
-          ws = *(const word*)p;
+          ws[into] = *(const word*)p;
         } else {
           uint32_t w = 0x7f7f7f7fu;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (2 * step + i < nb) w = (w & ~(0xffu << (8 * i))) | ((uint32_t)p[i] << (8 * i));
-          ws = w;
+          ws[into] = w;
         }
       }
     }
@@ -177,12 +181,13 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
   // the steps up to here lie inside x and W, and so do the loads of W that go with them
   const int64_t hot_end =
       min(min(last, inside_end), TR ? last : nb < 4 ? 0 : (nb - 4) / 2 + 1);
-  const auto store_w = [&](int64_t step) {
+  const auto store_w = [&](int64_t step, int from = 0) {
     char* const to = wlds + ((int)(step - first) >> (TR ? 0 : 1) & 1) * kWBytes;
     if constexpr (TR) {
       if (kThreads > kLoaders && tid >= kLoaders) return;
-      const float scale = mx4_scale(step * kStep + wrow < W.rows ? ws : 127u);
-      const uint32_t words[4] = {wr[0][0], wr[0][1], wr[0][2], wr[0][3]};
+      const float scale = mx4_scale(step * kStep + wrow < W.rows ? ws[from] : 127u);
+      const u32x4 c = wr[from][0];
+      const uint32_t words[4] = {c[0], c[1], c[2], c[3]};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int at = (4 * wblock + (i ^ ((wblock >> 2) & 3))) ^ ((wrow & 3) << 2);
@@ -192,9 +197,9 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
 #pragma unroll
       for (int i = 0; i < kW; ++i) {
         const int id = tid + i * kThreads, r = id / 4;
-        *(u32x4*)(to + r * 64 + 16 * ((id % 4) ^ ((r >> 2) & 3))) = wr[i];
+        *(u32x4*)(to + r * 64 + 16 * ((id % 4) ^ ((r >> 2) & 3))) = wr[from][i];
       }
-      if (BM == kThreads || tid < BM) *(uint32_t*)(to + BM * 64 + tid * 4) = ws;
+      if (BM == kThreads || tid < BM) *(uint32_t*)(to + BM * 64 + tid * 4) = ws[from];
     }
   };
 
@@ -260,7 +265,29 @@ __device__ __forceinline__ void tile_product(const Mx4MatmulArgs& a, const Tile&
     store_x(step);
   }
   __syncthreads();
-  if constexpr (!SB) {
+  if constexpr (kTwo) {
+    // (step + 1 is on its way already)
+    if (step + 3 < hot_end) {
+      load_x(step + 1, std::true_type(), 1);
+      load_w(step + 1, std::true_type(), 1);
+    }
+    for (; step + 3 < hot_end; step += 2) {
+      load_x(step + 2, std::true_type());
+      load_w(step + 2, std::true_type());
+      __builtin_amdgcn_sched_barrier(0);
+      products(step, std::integral_constant<int, 0>());
+      store_x(step + 1, 1);
+      store_w(step + 1, 1);
+      __syncthreads();
+      load_x(step + 3, std::true_type(), 1);
+      load_w(step + 3, std::true_type(), 1);
+      __builtin_amdgcn_sched_barrier(0);
+      products(step + 1, std::integral_constant<int, 1>());
+      store_x(step + 2);
+      store_w(step + 2);
+      __syncthreads();
+    }
+  } else if constexpr (!SB) {
     for (; step + 2 < hot_end; step += 2) {
       load_x(step + 1, std::true_type());
       load_w(step + (TR ? 1 : 2), std::true_type());
