@@ -404,7 +404,8 @@ struct Cut : Mx4Cut {
   int bm, bn;
 };
 // Large tiles (256 rows; transposed 256 tokens too) where they fill the GPU (4096 x 4096,
-// 2048 tokens: 76 us, 84 with small ones).  Fewer tiles than compute units are cut along
+// 2048 tokens: 76 us, 84 with small ones; gradient of 3000 tokens, 192 large tiles: 109 us,
+// 123 with small ones; of 2048, 128 tiles: 106 and 82).  Fewer tiles than compute units are cut along
 // the inner size until they do, in pieces of at least four steps (4096 x 4096, 256
 // tokens: 24.6 us in four pieces, 28.7 in eight, 42 whole: the pieces are written and
 // read again).  Of a few more than a round of them those past it are cut, so that they do
@@ -415,7 +416,7 @@ Cut cut(const Mx4& W, int transposed, int dtype, int64_t T) {
   const int64_t steps = cdiv(K, kStep);
   Cut c;
   const int64_t wide = transposed ? 256 : 128;
-  c.large = dtype != kF32 && cdiv(M, 256) * cdiv(T, wide) >= (transposed ? 128 : 256);
+  c.large = dtype != kF32 && cdiv(M, 256) * cdiv(T, wide) >= (transposed ? 160 : 256);
   c.bm = c.large ? 256 : 128;
   c.bn = c.large ? (int)wide : 128;
   c.tiles_m = (uint32_t)cdiv(M, c.bm);
