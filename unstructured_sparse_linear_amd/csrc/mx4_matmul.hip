@@ -409,8 +409,9 @@ struct Cut : Mx4Cut {
 // the inner size until they do, in pieces of at least four steps (4096 x 4096, 256
 // tokens: 24.6 us in four pieces, 28.7 in eight, 42 whole: the pieces are written and
 // read again).  Of a few more than a round of them those past it are cut, so that they do
-// not take a round of their own (2304 tokens: 84 us, 103 whole; gradient of 4352 tokens
-// 155 and 215).
+// not take a round of their own (2304 tokens, 32 tiles past it: 103 us whole, 81 in four
+// pieces, 85 in eight or two; gradient of 4352 tokens, 16 past it: 215 whole, 145 in eight
+// pieces, 154 in sixteen or four; of 5120, 64 past it: 172 in four, 180 in two).
 Cut cut(const Mx4& W, int transposed, int dtype, int64_t T) {
   const int64_t M = transposed ? W.cols : W.rows, K = transposed ? W.rows : W.cols;
   const int64_t steps = cdiv(K, kStep);
@@ -424,7 +425,12 @@ Cut cut(const Mx4& W, int transposed, int dtype, int64_t T) {
   const int64_t tiles = (int64_t)c.tiles_m * c.tiles_n, rest = tiles % kSlots;
   // the transposed large tiles have a compute unit each, others share one
   const int64_t few = tiles < kSlots ? (c.large ? 0 : kSlots) : c.large && transposed ? 128 : 85;
-  const int64_t pieces = rest > 0 && rest <= few ? std::min<int64_t>(kSlots / rest, steps / 4) : 1;
+  int64_t pieces = 1;
+  if (rest > 0 && rest <= few) {
+    pieces = kSlots / rest;
+    if (tiles > kSlots) pieces = std::max(std::min<int64_t>(pieces, 4), kSlots / 2 / rest);
+    pieces = std::min(pieces, steps / 4);
+  }
   c.whole = (uint32_t)(pieces > 1 ? tiles - rest : tiles);
   c.steps = (int32_t)cdiv(steps, std::max<int64_t>(pieces, 1));
   c.pieces = (uint32_t)cdiv(steps, c.steps);
