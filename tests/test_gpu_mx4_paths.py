@@ -273,3 +273,14 @@ def test_example():
     for t in range(5):
         want[:, t] += B[t % 3] @ (A[t % 3] @ xt[:, t])
     assert np.abs(step.double().cpu().numpy() - want).max() < 1e-5 * np.abs(want).max()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1919, 300), (1921, 300), (2301, 33), (4100, 1000)])
+def test_quantising_along_columns(dtype, rows, cols):
+    """Few and many tiles of rows, each in its own order: the same bits as along the rows."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    big = torch.randn(cols, rows + 1, generator=g, device="cuda").to(ref.DTYPES[dtype])
+    x = big[:, 1:].t()
+    got, want = S.mx4_quantize(x), S.mx4_quantize(x.contiguous())
+    assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)

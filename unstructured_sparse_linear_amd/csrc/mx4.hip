@@ -5,7 +5,7 @@
 //
 // Both directions are bound by memory: 11008 x 4096 bf16 quantised in 22.3 us (5.1 TB/s),
 // dequantised in 17.8 (6.4, part of it in the memory-side cache); 2047 tokens x 4096 of
-// f16 along the columns in 10.2 and 5.4.
+// f16 along the columns in 9.3 and 5.4.
 #include <algorithm>
 
 #include "kernels.h"
@@ -55,7 +55,11 @@ __global__ __launch_bounds__(kThreads) void mx4_quantize_rows(const T* w, int64_
 // features): 128 rows (tokens) x 8 blocks a workgroup, a wave a block.  A lane holds the
 // 32 elements of two neighbouring rows, so that a load of the wave is 256 neighbouring
 // bytes and a block's maximum needs no other lane; codes go through shared memory, so
-// that a row's eight blocks are stored as one line.
+// that a row's eight blocks are stored as one line.  Neighbouring workgroups take
+// neighbouring rows: in the other order, columns a power of two apart meet in few memory
+// channels (8192 tokens x 4096, bf16: 13.7 us, 16.3 so).  Where there are few of them,
+// neighbours share an XCD, as lines cross tiles (300 tokens x 4096 and their product of
+// two: 20.9 us, 21.7 apart; 8192 tokens: 16.0).
 constexpr int kTileRows = 128, kTileBlocks = 8;
 template <typename T>
 __global__ __launch_bounds__(64 * kTileBlocks) void mx4_quantize_columns(const T* w, int64_t rows,
@@ -68,8 +72,9 @@ __global__ __launch_bounds__(64 * kTileBlocks) void mx4_quantize_columns(const T
   __shared__ __attribute__((aligned(16))) char lds[kTileRows * kRow];
   __shared__ __attribute__((aligned(8))) uint8_t bytes[kTileRows * kTileBlocks];
   const int64_t nb = (cols + kMx4Block - 1) / kMx4Block;
-  const int64_t r0 = (int64_t)(blockIdx.x / tiles) * kTileRows;
-  const int64_t b0 = (int64_t)(blockIdx.x % tiles) * kTileBlocks;
+  const uint32_t index = tiles < 16 ? xcd_index(blockIdx.x, gridDim.x) : blockIdx.x;
+  const int64_t r0 = (int64_t)(index % tiles) * kTileRows;
+  const int64_t b0 = (int64_t)(index / tiles) * kTileBlocks;
   const int tid = threadIdx.x, lane = tid % 64, wave = wave_uniform(tid / 64);
   const int64_t r = r0 + 2 * lane, k0 = (b0 + wave) * kMx4Block;
   if (k0 < cols) {
@@ -206,9 +211,9 @@ hipError_t quantize(const void* w, int64_t rows, int64_t cols, int64_t rs, int64
       mx4_quantize_rows<T><<<(uint32_t)cdiv(n * 4 * nb, kThreads), kThreads, 0, s>>>(
           from, n, cols, rs, (uint32_t*)c, scales + r * nb);
     } else {
-      const uint32_t tiles = (uint32_t)cdiv(nb, kTileBlocks);
+      const uint32_t tiles = (uint32_t)cdiv(n, kTileRows);
       mx4_quantize_columns<T>
-          <<<(uint32_t)cdiv(n, kTileRows) * tiles, 64 * kTileBlocks, 0, s>>>(from, n, cols, cs, tiles,
+          <<<(uint32_t)cdiv(nb, kTileBlocks) * tiles, 64 * kTileBlocks, 0, s>>>(from, n, cols, cs, tiles,
                                                                             c, scales + r * nb);
     }
   }
