@@ -245,8 +245,16 @@ class LowRankAdapters(torch.nn.Module):
     With dropout = p, forward in training drops elements of xt on the adapters' side
     (not in yt) with probability p.  The masks follow from `dropout_state`, an int64
     buffer of a seed and a step that each such call advances on the device; seed
-    defaults to a number of torch's generator.  A forward pass that is run again (for
-    activations that were not kept) has to start from the same dropout_state."""
+    defaults to a number of torch's generator.  A forward pass that is run again in the
+    backward pass (for activations that were not kept) needs the mask it had: take the
+    state before, and give it to both:
+
+      checkpoint(layer, yt, xt, offsets, adapter, layer.next_dropout_state())
+
+    Without it such a pass raises, unless dropout_state was set back by hand."""
+
+    # the version of dropout_state that next_dropout_state left
+    _dropout_version: Optional[int] = None
 
     def __init__(self, adapters: int, rank: int, in_features: int, out_features: int,
                  scale: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None,
@@ -279,13 +287,27 @@ class LowRankAdapters(torch.nn.Module):
             self.scale = scale.to(self.scale.device)
         return self
 
+    def next_dropout_state(self) -> Optional[torch.Tensor]:
+        """The seed and step of the next forward pass in training, a copy that forward
+        takes as `state`; dropout_state advances.  None where nothing is dropped."""
+        if not (self.training and self.dropout > 0.0):
+            return None
+        at = self.dropout_state
+        # a pass that is run again here would draw the mask of another step
+        if torch._C._current_graph_task_id() != -1 and _version(at) == self._dropout_version:
+            raise RuntimeError("a forward pass with dropout inside a backward pass draws another "
+                               "mask; take next_dropout_state() before and give it as state")
+        state = at.clone()
+        at[1].add_(1)
+        self._dropout_version = _version(at)
+        return state
+
     def forward(self, yt: torch.Tensor, xt: torch.Tensor, offsets: torch.Tensor,
-                adapter: torch.Tensor) -> torch.Tensor:
+                adapter: torch.Tensor, state: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """`state`: of next_dropout_state, which is called where none is given."""
         if self.training and self.dropout > 0.0:
-            # the backward pass draws the mask again from a copy of the state
-            state = self.dropout_state.clone()
-            self.dropout_state[1].add_(1)
-            xt = dropout(xt, self.dropout, state)
+            # the backward pass draws the mask again from the state, which is a copy
+            xt = dropout(xt, self.dropout, self.next_dropout_state() if state is None else state)
         return low_rank_linear(yt, xt, self.A, self.B, offsets, adapter, self.scale, self.ranks)
 
     @torch.no_grad()
@@ -296,6 +318,10 @@ class LowRankAdapters(torch.nn.Module):
             return low_rank_add(yt, xt, self.A, self.B, offsets, adapter, self.scale, self.ranks,
                                 out=yt)
         return low_rank_project(W, xt, self.A, self.B, offsets, adapter, self.scale, self.ranks)
+
+
+def _version(t: torch.Tensor) -> int:
+    return -1 if t.is_inference() else t._version
 
 
 class MaskedAdam(torch.optim.Optimizer):
