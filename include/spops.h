@@ -561,9 +561,9 @@ spops_status spops_mx4_dequantize(const spops_mx4* W, void* out, spops_dtype dty
  * out = W^T x for x [rows][tokens], out [cols][tokens] (the gradient of the input).
  * x and out have the type dtype and unit stride along the tokens.  Every product is
  * exact, sums are f32, and each output is rounded once (bits of an f32 x below 2^-133
- * are left out).  tokens in 0..2^30; out of at most 2^23 tiles of 128 x 128.  out
- * overlaps no input.  The workspace is 256-byte aligned (NULL where its size is 0) and
- * needs no preparation. */
+ * are left out).  tokens in 0..2^30; out of at most 2^23 tiles of 128 x 128 (f32:
+ * 2^23 - 1).  out overlaps no input.  The workspace is 256-byte aligned (NULL where its
+ * size is 0) and needs no preparation. */
 spops_status spops_mx4_matmul_workspace_size(const spops_mx4* W, int transposed,
                                              spops_dtype dtype, int64_t tokens, size_t* bytes);
 spops_status spops_mx4_matmul(const spops_mx4* W, int transposed, const void* x,
@@ -571,7 +571,7 @@ spops_status spops_mx4_matmul(const spops_mx4* W, int transposed, const void* x,
                               int64_t ldo, void* workspace, size_t workspace_bytes,
                               void* hip_stream);
 /* out [W.rows][X.rows] = W X^T with both in four bits (X: tokens x cols): exact
- * products, f32 sums, one rounding to dtype. */
+ * products, f32 sums, one rounding to dtype; out of at most 2^23 tiles of 128 x 128. */
 spops_status spops_mx4_matmul4_workspace_size(const spops_mx4* W, int64_t tokens, size_t* bytes);
 spops_status spops_mx4_matmul4(const spops_mx4* W, const spops_mx4* X, void* out,
                                spops_dtype dtype, int64_t ldo, void* workspace,

@@ -1093,10 +1093,12 @@ spops_status check_mx4(const spops_mx4* W) {
   return SPOPS_OK;
 }
 Mx4 mx4_of(const spops_mx4* W) { return {W->rows, W->cols, W->codes, W->scales}; }
-// Tiles of an output are counted in 32 bits, and so are their threads (of any memory
-// the outputs of the sizes that are refused take the whole).
-bool mx4_output(int64_t rows, int64_t tokens) {
-  return ((rows + 127) / 128) * ((tokens + 127) / 128) <= (1 << 23);
+// An output's tiles of 128 x 128: up to 2^23, of f32 activations, whose tiles have 512
+// threads, fewer, as a launch has fewer than 2^32 threads (of 16 bits 256 at most for
+// each, larger tiles included).
+bool mx4_output(int64_t rows, int64_t tokens, bool f32) {
+  const int64_t tiles = ((rows + 127) / 128) * ((tokens + 127) / 128);
+  return tiles <= (1 << 23) - (f32 ? 1 : 0);
 }
 spops_status workspace_ok(const void* ws, size_t have, size_t want) {
   if (want > 0 && (!ws || have < want || ((uintptr_t)ws & 255))) return SPOPS_ERR_WORKSPACE;
@@ -1135,7 +1137,7 @@ spops_status spops_mx4_matmul_workspace_size(const spops_mx4* W, int transposed,
   if (!dtype_ok(dtype)) return SPOPS_ERR_DTYPE;
   if (!W || !bytes) return SPOPS_ERR_NULL;
   if (!mx4_size(W->rows, W->cols) || tokens < 0 || tokens > kMx4MaxTokens ||
-      !mx4_output(transposed ? W->cols : W->rows, tokens))
+      !mx4_output(transposed ? W->cols : W->rows, tokens, dtype == SPOPS_F32))
     return SPOPS_ERR_SHAPE;
   *bytes = tokens == 0 ? 0 : mx4_matmul_bytes(mx4_of(W), transposed != 0, dtype, tokens);
   return SPOPS_OK;
@@ -1150,7 +1152,7 @@ spops_status spops_mx4_matmul(const spops_mx4* W, int transposed, const void* x,
   if (st != SPOPS_OK) return st;
   const Mx4 w = mx4_of(W);
   if (tokens < 0 || tokens > kMx4MaxTokens || ldx < tokens || ldo < tokens ||
-      !mx4_output(transposed ? w.cols : w.rows, tokens))
+      !mx4_output(transposed ? w.cols : w.rows, tokens, dtype == SPOPS_F32))
     return SPOPS_ERR_SHAPE;
   if (tokens == 0) return SPOPS_OK;
   if (!x || !out) return SPOPS_ERR_NULL;
@@ -1170,7 +1172,7 @@ spops_status spops_mx4_matmul(const spops_mx4* W, int transposed, const void* x,
 spops_status spops_mx4_matmul4_workspace_size(const spops_mx4* W, int64_t tokens, size_t* bytes) {
   if (!W || !bytes) return SPOPS_ERR_NULL;
   if (!mx4_size(W->rows, W->cols) || tokens < 0 || tokens > kMx4MaxSize ||
-      !mx4_output(W->rows, tokens))
+      !mx4_output(W->rows, tokens, false))
     return SPOPS_ERR_SHAPE;
   *bytes = tokens == 0 ? 0 : mx4_matmul4_bytes(mx4_of(W), tokens);
   return SPOPS_OK;
@@ -1183,7 +1185,8 @@ spops_status spops_mx4_matmul4(const spops_mx4* W, const spops_mx4* X, void* out
   spops_status st = check_mx4(W);
   if (st == SPOPS_OK) st = check_mx4(X);
   if (st != SPOPS_OK) return st;
-  if (X->cols != W->cols || ldo < X->rows || !mx4_output(W->rows, X->rows)) return SPOPS_ERR_SHAPE;
+  if (X->cols != W->cols || ldo < X->rows || !mx4_output(W->rows, X->rows, false))
+    return SPOPS_ERR_SHAPE;
   if (!out) return SPOPS_ERR_NULL;
   const Mx4 w = mx4_of(W);
   st = workspace_ok(workspace, workspace_bytes, mx4_matmul4_bytes(w, X->rows));
