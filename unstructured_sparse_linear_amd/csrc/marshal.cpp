@@ -596,10 +596,10 @@ PyObject* dropout(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const at::Tensor out = into ? THPVariable_Unpack(args[4]) : at::empty(x.sizes(), x.options());
     const int64_t ldo = rows_of(out, "out", out_rows, out_cols);
     if (into && x.numel() && !(out.data_ptr() == x.data_ptr() && (rows <= 1 || ldo == ldx))) {
-      const auto end = [&](const at::Tensor& t, int64_t ld) {
-        return (const char*)t.data_ptr() + ((rows - 1) * ld + cols) * t.element_size();
-      };
-      need((const char*)out.data_ptr() >= end(x, ldx) || (const char*)x.data_ptr() >= end(out, ldo),
+      // (others than matrices are contiguous, as long as x is)
+      const char *const a = (const char*)x.data_ptr(), *const b = (const char*)out.data_ptr();
+      const int64_t bytes = x.numel() * x.element_size();
+      need(x.dim() == 2 ? !columns_meet(x, ldx, out, ldo) : b >= a + bytes || a >= b + bytes,
            "out", "must be x or not overlap it");
     }
     status("spops_dropout", spops_dropout(x.data_ptr(), dt, rows, cols, ldx, out.data_ptr(), ldo, p,
