@@ -113,6 +113,19 @@ class SparseAdapter(torch.nn.Module):
         return csr_add(self.values.detach(), P.ro, P.ri, P.ci, W)
 
 
+def _apply_keeping(module, types, apply, fn, *args, **kwargs):
+    """Moves and casts of a module (apply: torch.nn.Module._apply, by which type() reaches
+    integers too): the buffers in `types` move, but keep the type given there, with the
+    values they had."""
+    kept = {n: module._buffers[n] for n in types if module._buffers.get(n) is not None}
+    apply(fn, *args, **kwargs)
+    for n, t in kept.items():
+        now = module._buffers[n]
+        if now.dtype != types[n]:
+            module._buffers[n] = t.to(now.device)
+    return module
+
+
 class _Mx4LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, xt, codes, scales, cols, transposed):
@@ -149,6 +162,10 @@ class Mx4Linear(torch.nn.Module):
     @property
     def weight(self) -> Mx4Matrix:
         return Mx4Matrix(self.codes, self.scales, self.cols)
+
+    def _apply(self, fn, *args, **kwargs):
+        types = {"codes": torch.uint8, "scales": torch.uint8}
+        return _apply_keeping(self, types, super()._apply, fn, *args, **kwargs)
 
     def forward(self, xt: torch.Tensor) -> torch.Tensor:
         return _Mx4LinearFn.apply(xt, self.codes, self.scales, self.cols, False)
@@ -279,13 +296,8 @@ class LowRankAdapters(torch.nn.Module):
                                  torch.tensor([seed, 0], dtype=torch.int64, device=device))
 
     def _apply(self, fn, *args, **kwargs):
-        """Moves and casts of the module: scale moves, but stays float32 with the
-        values it had."""
-        scale = self.scale
-        super()._apply(fn, *args, **kwargs)
-        if scale is not None and self.scale.dtype != torch.float32:
-            self.scale = scale.to(self.scale.device)
-        return self
+        types = {"scale": torch.float32, "ranks": torch.int32, "dropout_state": torch.int64}
+        return _apply_keeping(self, types, super()._apply, fn, *args, **kwargs)
 
     def next_dropout_state(self) -> Optional[torch.Tensor]:
         """The seed and step of the next forward pass in training, a copy that forward
