@@ -150,7 +150,8 @@ class Mx4Linear(torch.nn.Module):
     """A frozen layer of out_features x in_features in 4-bit microscaled form:
     forward(X^T) = W · X^T in the dtype of X^T, differentiable in X^T.  `weight` is a
     matrix to quantise or an Mx4Matrix.  Adapters train on top of it:
-    adapters(base(xt), xt, offsets, adapter)."""
+    adapters(base(xt), xt, offsets, adapter).  A state of another number of columns does
+    not load, also where codes and scales have the same shapes."""
 
     def __init__(self, weight: Union[torch.Tensor, Mx4Matrix]):
         super().__init__()
@@ -162,6 +163,31 @@ class Mx4Linear(torch.nn.Module):
     @property
     def weight(self) -> Mx4Matrix:
         return Mx4Matrix(self.codes, self.scales, self.cols)
+
+    def state_dict(self, *args, **kwargs):
+        """codes and scales; the number of columns, which they do not tell, goes with them
+        as the version of a module does."""
+        state = super().state_dict(*args, **kwargs)
+        prefix = kwargs.get("prefix", args[1] if len(args) > 1 else "")
+        getattr(state, "_metadata", {}).get(prefix[:-1], {})["cols"] = self.cols
+        return state
+
+    def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys,
+                              unexpected_keys, error_msgs):
+        cols, codes = local_metadata.get("cols", self.cols), state_dict.get(prefix + "codes")
+        if cols != self.cols:
+            error_msgs.append(f"{prefix}codes are of {cols} columns, those of the layer of "
+                              f"{self.cols}.")
+            return
+        if (isinstance(codes, torch.Tensor) and codes.shape == self.codes.shape
+                and not codes.is_meta):
+            # without that number: what lies past the last column has to be zero
+            past = codes[:, (self.cols + 1) // 2:]
+            if past.any() or self.cols % 2 and (codes[:, self.cols // 2] > 15).any():
+                error_msgs.append(f"{prefix}codes hold elements past column {self.cols}.")
+                return
+        super()._load_from_state_dict(state_dict, prefix, local_metadata, strict, missing_keys,
+                                      unexpected_keys, error_msgs)
 
     def _apply(self, fn, *args, **kwargs):
         types = {"codes": torch.uint8, "scales": torch.uint8}
