@@ -325,10 +325,15 @@ class LowRankAdapters(torch.nn.Module):
         types = {"scale": torch.float32, "ranks": torch.int32, "dropout_state": torch.int64}
         return _apply_keeping(self, types, super()._apply, fn, *args, **kwargs)
 
+    def _drops(self) -> bool:
+        # the constructor's own number: a module that was kept whole before it had one has
+        # none, and a class made from this one may have a layer of that name
+        return self.training and self.__dict__.get("dropout", 0.0) > 0.0
+
     def next_dropout_state(self) -> Optional[torch.Tensor]:
         """The seed and step of the next forward pass in training, a copy that forward
         takes as `state`; dropout_state advances.  None where nothing is dropped."""
-        if not (self.training and self.dropout > 0.0):
+        if not self._drops():
             return None
         at = self.dropout_state
         # a pass that is run again here would draw the mask of another step
@@ -343,7 +348,7 @@ class LowRankAdapters(torch.nn.Module):
     def forward(self, yt: torch.Tensor, xt: torch.Tensor, offsets: torch.Tensor,
                 adapter: torch.Tensor, state: Optional[torch.Tensor] = None) -> torch.Tensor:
         """`state`: of next_dropout_state, which is called where none is given."""
-        if self.training and self.dropout > 0.0:
+        if self._drops():
             # the backward pass draws the mask again from the state, which is a copy
             xt = dropout(xt, self.dropout, self.next_dropout_state() if state is None else state)
         return low_rank_linear(yt, xt, self.A, self.B, offsets, adapter, self.scale, self.ranks)
