@@ -223,7 +223,8 @@ def dropout(x: torch.Tensor, p: float, seed: Union[int, torch.Tensor], step: int
     dimension are the columns.  An element is dropped when 16 random bits of it are
     below limit = round(65536 p), and kept ones are scaled by 65536 / (65536 - limit).
     `seed` is a number or an int64 vector of seed and step on the device, which is read
-    when the kernel runs (a captured call then takes what it holds at each replay).
+    when the kernel runs (a captured call then takes what it holds at each replay; `step`
+    is not used).
     Differentiable in x (the gradient is the same call on dy; a vector `seed` must not
     change before it; forward mode raises), unless `out` is given, which may be x."""
     if out is not None:
@@ -287,8 +288,10 @@ class LowRankAdapters(torch.nn.Module):
 
     With dropout = p, forward in training drops elements of xt on the adapters' side
     (not in yt) with probability p.  The masks follow from `dropout_state`, an int64
-    buffer of a seed and a step that each such call advances on the device; seed
-    defaults to a number of torch's generator.  A forward pass that is run again in the
+    buffer of a seed and a step that each such call advances on the device.  Modules of
+    equal seeds and input sizes draw equal masks at a step: each layer, and each rank of a
+    data-parallel job, needs a seed of its own (which a broadcast of buffers undoes).  By
+    default it is a number of torch's generator.  A forward pass that is run again in the
     backward pass (for activations that were not kept) needs the mask it had: take the
     state before, and give it to both:
 
