@@ -23,7 +23,7 @@ from __future__ import annotations
 from typing import Optional, Union
 
 import torch
-from torch.autograd.forward_ad import unpack_dual
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from .spops import (Mx4Matrix, SddmmPlan, SpmmPlan, _marshal, csr_add, csr_transpose_permutation,
@@ -228,17 +228,18 @@ def dropout(x: torch.Tensor, p: float, seed: Union[int, torch.Tensor], step: int
     Differentiable in x (the gradient is the same call on dy; a vector `seed` must not
     change before it; forward mode raises), unless `out` is given, which may be x."""
     if out is not None:
-        if any(torch.is_grad_enabled() and t.requires_grad or _has_tangent(t) for t in (x, out)):
+        if any(t.requires_grad and torch.is_grad_enabled() or _has_tangent(t) for t in (x, out)):
             raise ValueError("dropout into out has no gradient; detach x")
         return _marshal().dropout(x, p, seed, step, out)
-    if torch.is_grad_enabled() and x.requires_grad or _has_tangent(x):
+    if x.requires_grad and torch.is_grad_enabled() or _has_tangent(x):
         return _DropoutFn.apply(x, p, seed, step)
     return _marshal().dropout(x, p, seed, step, None)
 
 
 def _has_tangent(t: torch.Tensor) -> bool:
-    """Whether t is a dual tensor, whose tangent only an autograd function can refuse."""
-    return unpack_dual(t).tangent is not None
+    """Whether t is a dual tensor, whose tangent only an autograd function can refuse.  (The
+    level is looked at first: unpack_dual alone is 0.4 us of a call of 4.5.)"""
+    return forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None
 
 
 class _LowRankLinearFn(torch.autograd.Function):
