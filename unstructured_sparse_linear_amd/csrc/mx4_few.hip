@@ -1,7 +1,8 @@
 // mx4_few.hip -- products of a 4-bit microscaled matrix with the few tokens of a
 // decode step, out = W x.
 //
-// Bound by reading W once.  A workgroup of eight waves makes 16 RT rows of W times up
+// W is read once, which bounds a single token; with more, x is brought again by every
+// workgroup and staged by each wave for itself.  A workgroup of eight waves makes 16 RT rows of W times up
 // to 16 NT tokens; the waves take turns at slabs of 128 k, so that together they read
 // 512 neighbouring bytes of each row, and add their sums through shared memory at the
 // end.  In a slab, lanes 16 g + r hold block g of row r: 16 bytes, one scale, four
@@ -13,8 +14,9 @@
 // a token are read turned; a single token's x needs no turning and is loaded as it
 // is.
 //
-// 4096 x 4096 in bf16: one token 4.4 us (a launch that only reads W 2.3, an empty one
-// 1.6), 16 tokens 5.6; 4096 -> 11008: one 7.8 (only reading 4.4), 32 tokens of f16 11.4.
+// 4096 x 4096 in bf16: one token 4.3 to 4.9 us (a launch that only reads W 2.3 to 2.6, an
+// empty one 1.6), 16 tokens 5.6; 4096 -> 11008: one 7.8 (only reading 4.4 to 5.0), 32 tokens
+// of f16 11.4.
 #include <algorithm>
 #include <type_traits>
 

@@ -21,7 +21,7 @@
 // 1024 tokens 65 us, so 52.)  W^T x converts W into shared memory and reads it turned.
 //
 // Bound by the matrix cores at the clock that their power leaves: with operands of
-// random bits they reach 1.65 PFLOP/s and no more.  8192 tokens, 4096 -> 11008, bf16:
+// random bits they reach 1.69 PFLOP/s and no more.  8192 tokens, 4096 -> 11008, bf16:
 // 643 us, 1.15 PFLOP/s (a library's dense bf16 product of that size 701); gradient of
 // 4096 tokens, 4096 x 4096: 118 us, 1.16.
 #include <algorithm>

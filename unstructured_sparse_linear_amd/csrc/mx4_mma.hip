@@ -7,9 +7,11 @@
 //
 // A step of 256 k takes whole lines (128 bytes) of each row's codes through shared
 // memory, and scales come for two steps at a time.  8192 tokens, 4096 -> 11008, bf16 out:
-// 290 us, 2.5 PFLOP/s (the matrix cores reach 5.9 on random operands); its steps are so
-// short that barriers and shared memory bound it.  300 tokens, 4096 x 4096: 15.4 us,
-// bound by the chain of a tile's steps.
+// 290 us, 2.5 PFLOP/s (the matrix cores reach 6.0 on random operands, and are busy for
+// 26% of the cycles): one workgroup a compute unit, whose steps are a few hundred clocks
+// between barriers and whose output nothing overlaps.  Bytes do not bound it (1.5 GB from
+// the L2s, 64 us at their 24 TB/s).  300 tokens, 4096 x 4096: 15.4 us, bound by the chain
+// of a tile's steps.
 #include <algorithm>
 #include <type_traits>
 
@@ -244,10 +246,11 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void mx4_mma_kernel(Args a, M
 struct Cut : Mx4Cut {
   int side;
 };
-// Tiles of 256, 128 or 64 square, the largest that fill the GPU (4096 x 4096, 1024
-// tokens: 21.8 us with 128, 24.4 with 64; 512: 18.9 and 17.7, 128: 17.1 and 12.6); few
-// small ones are cut along the inner size, in pieces of at least four steps, which two
-// groups of waves make (64 tokens: 9.2 us, 10.3 in pieces for four groups).
+// Tiles of 256, 128 or 64 square, the largest that fill the GPU (4096 x 4096, 2560
+// tokens: 43.5 us with 256, 46.0 with 128; 2048: 51.9 and 31.5; 1024: 22.2 with 128, 26.7
+// with 64; 640: 20.9 and 22.2; 512: 21.9 and 15.1; 128: 13.4 and 11.0); few small ones are
+// cut along the inner size, in pieces of at least four steps, which two groups of waves
+// make (64 tokens: 9.0 us, 10.3 in pieces for four groups).
 Cut cut(const Mx4& W, int64_t T) {
   const int64_t steps = cdiv(W.cols, kStep);
   Cut c;
